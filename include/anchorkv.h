@@ -323,6 +323,139 @@ int anchorkv_decode_attn_noalloc(const anchorkv_params* p, const void* compresse
                                  int32_t tail_cap, float* out, void* stream);
 
 /*
+ * Pages of the exact tail.
+ *
+ * The tokens appended during decode may be kept in pages instead of one dense
+ * tail per sequence: a pool of `n_pages` pages of `page_size` tokens, shared
+ * by `n_slots` sequences and by all layers of a model (one page table, one
+ * pool slice per layer).
+ *   K_pages, V_pages  device [n_layers][n_pages][H][page_size][D] dtype,
+ *                     16-byte aligned, two separate buffers
+ *   state             device int32, anchorkv_pages_state_bytes bytes:
+ *     header   [16]   0: status word (0 = ok), 1: free pages n_free, rest 0
+ *     free     [n_pages]   ids of the free pages, n_free of them (the last is
+ *                          handed out next), then -1
+ *     refs     [n_pages]   sequences that hold the page
+ *     len      [n_slots]   exact tokens of each sequence
+ *     table    [n_slots][max_pages]  its pages in order, then -1
+ * Token t of a sequence is row t % page_size of its page t / page_size.  A
+ * page that several sequences hold is full: a partly filled page has one
+ * owner, so appending never has to copy.
+ * The three operations below read `state_in` and write `state_out` (which may
+ * be the same buffer, else one of the same size), move rows of every layer's
+ * keys and values, and take effect whole or not at all: where the device
+ * finds that an operation cannot be done, the status word of state_out keeps
+ * the first code (1: too few free pages, 2: a page table is full, 3: an
+ * argument or a table entry out of its range) and nothing else changes.  The
+ * word stays set until anchorkv_pages_init; anchorkv_read_device_status reads
+ * it.  Which pages are handed out depends on the state alone.
+ */
+typedef struct anchorkv_pages {
+  int32_t n_pages;      /* 1..2^20                                            */
+  int32_t page_size;    /* tokens per page: 16, 32, 64 or 128                 */
+  int32_t n_slots;      /* sequences, 1..4096                                 */
+  int32_t max_pages;    /* page-table entries per sequence, 1..65536          */
+  int32_t n_layers;     /* layers sharing the page table, 1..1024             */
+  int32_t n_kv_heads;   /* H, 1..1024                                         */
+  int32_t head_dim;     /* D, must be 128                                     */
+  int32_t dtype;        /* anchorkv_dtype                                     */
+} anchorkv_pages;
+
+/* Bytes of a page state, and of the scratch the operations need.  Host, pure. */
+int anchorkv_pages_state_bytes(const anchorkv_pages* pg, size_t* bytes);
+int anchorkv_pages_workspace_bytes(const anchorkv_pages* pg, size_t* bytes);
+
+/* Makes every page free (handed out from page 0 up) and every sequence empty. */
+int anchorkv_pages_init(const anchorkv_pages* pg, int32_t* state, void* stream);
+
+/*
+ * Appends to sequence b (b < batch <= n_slots) the rows path[b][0 ..
+ * n_accept[b]) of its `n_draft` drafted tokens, in that order: what a
+ * verified path of a draft tree, or one decoded token, leaves in the cache.
+ *   K_new, V_new  device [n_layers][batch][n_draft][H][D] dtype
+ *   path          device [batch][n_draft] int32, or NULL for 0, 1, 2, ...
+ *                 (entries at n_accept[b] and behind are not read)
+ *   n_accept      device [batch] int32, 0..n_draft
+ * Fresh pages are handed out in the order of the sequences.
+ */
+int anchorkv_pages_commit(const anchorkv_pages* pg, const int32_t* state_in, int32_t* state_out,
+                          void* K_pages, void* V_pages, const void* K_new, const void* V_new,
+                          int32_t batch, int32_t n_draft, const int32_t* path,
+                          const int32_t* n_accept, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Makes sequence s a copy of what sequence parents[s] was (-1: empty), for
+ * all s at once: beams that are duplicated, reordered or dropped, and
+ * sequences that end.  Full pages are shared; of the copies of one sequence
+ * the one in the lowest slot keeps its partly filled page, the others get a
+ * page of their own with its rows (rows behind the last token stay as they
+ * were).  Pages that nobody holds any more become free first, in ascending
+ * order, then the new ones are handed out in the order of the slots.
+ *   parents  device [n_slots] int32
+ */
+int anchorkv_pages_fork(const anchorkv_pages* pg, const int32_t* state_in, int32_t* state_out,
+                        void* K_pages, void* V_pages, const int32_t* parents, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * Moves the pages in use to the front of the pool: with n of them in use, the
+ * i-th used page at n or behind goes to the i-th free page below n.  Pages n
+ * and up are free afterwards (handed out from n up), so the pool can be cut
+ * there or its front copied as one block.
+ */
+int anchorkv_pages_compact(const anchorkv_pages* pg, const int32_t* state_in, int32_t* state_out,
+                           void* K_pages, void* V_pages, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention for a tree of drafted tokens over compressed caches: draft t of
+ * sequence b attends to
+ *   - the N compressed tokens of its layout (K^, V^ as anchorkv_decode_attn
+ *     rebuilds them),
+ *   - the exact tokens of its pages,
+ *   - the drafts i < n_new[b] whose bit i is set in mask[b][t] (its ancestors
+ *     in the tree and, as a rule, itself),
+ * with logits q . k / sqrt(D).  One draft is single-token decoding with a
+ * paged tail.  A draft that sees nothing at all gives zeros; infinities and
+ * NaN in drafts that it does not see do not reach it.
+ */
+typedef struct anchorkv_tree {
+  int32_t batch;             /* sequences                                     */
+  int32_t n_draft;           /* T, drafts per sequence, 1..64                 */
+  const void* compressed;    /* device, n_layouts layouts one every seq_stride_bytes; NULL: no compressed tokens */
+  int64_t seq_stride_bytes;  /* >= total_bytes, a multiple of 16              */
+  int32_t n_layouts;
+  const int32_t* layout_of;  /* device [batch], the layout of each sequence (beams share one), or NULL for b */
+  const void* q;             /* device [batch][T][H_q][D] dtype with the strides below */
+  int64_t q_seq_stride, q_tok_stride;          /* in elements                 */
+  const void* K_new;         /* device [batch][T][H][D] dtype, the drafts' keys and values */
+  const void* V_new;
+  int64_t new_seq_stride, new_tok_stride;      /* in elements, of both        */
+  const int32_t* n_new;      /* device [batch], 0..T drafts of each sequence, or NULL for T */
+  const uint64_t* mask;      /* device [batch][T], or NULL for a chain (draft t sees 0..t) */
+  const anchorkv_pages* pages;                 /* NULL: no exact tokens       */
+  const int32_t* state;      /* device page state, slot b = sequence b        */
+  const void* K_pages;       /* this layer's slice [n_pages][H][page_size][D] */
+  const void* V_pages;
+  void* out;                 /* device [batch][T][H_q][D] dtype; rows t >= n_new[b] stay as they are */
+} anchorkv_tree;
+
+/* Workspace bytes anchorkv_tree_attn needs for `batch` sequences of `n_draft`
+ * drafts; pg may be NULL (no exact tokens).  Host, pure. */
+int anchorkv_tree_workspace_bytes(const anchorkv_params* p, int32_t batch, int32_t n_draft,
+                                  const anchorkv_pages* pg, size_t* ws_bytes);
+
+/*
+ * Runs the attention above on `stream`.  Every device pointer is 16-byte
+ * aligned, and so is every row that the strides reach (EINVAL otherwise); D is
+ * contiguous and heads are D apart.  The call overwrites `ws`, whose first
+ * words are a status word and counters: a layout_of or page-table entry out of
+ * its range latches code 3 there (anchorkv_read_device_status) and the rows of
+ * that sequence become NaN.  EUNSUPPORTED when batch * H > 65535 or the page
+ * tables reach more than 2^20 tokens.
+ */
+int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Test and inspection hook: writes the dense reconstruction
  * x^_t = gamma~_t x_a(t) + r~_t of one compressed layer.
  *   K_hat, V_hat device [H][N][D] float32.
@@ -350,7 +483,7 @@ int anchorkv_codebook(double* out4);
 int anchorkv_stage_timing(int enable);
 
 /* Number of timed stages reported by anchorkv_stage_times. */
-#define ANCHORKV_N_STAGES 16
+#define ANCHORKV_N_STAGES 18
 
 /* Waits for the recorded events and returns, per stage (n >= ANCHORKV_N_STAGES entries),
  * the accumulated milliseconds and the number of timed calls since the last

@@ -259,6 +259,235 @@ def decode_attn_noalloc(p: AnchorKVParams, compressed: torch.Tensor, q: torch.Te
     return out
 
 
+@dataclass
+class PageSpec:
+    """Sizes of a page pool of exact decode-time tokens (anchorkv_pages): the
+    pool tensors are [n_layers, n_pages, n_kv_heads, page_size, head_dim]."""
+    n_pages: int
+    page_size: int = 64
+    n_slots: int = 1
+    max_pages: int = 64
+    n_layers: int = 1
+    n_kv_heads: int = 8
+    dtype: str = "bf16"
+    head_dim: int = 128
+
+    def c(self) -> capi.Pages:
+        return capi.Pages(self.n_pages, self.page_size, self.n_slots, self.max_pages, self.n_layers, self.n_kv_heads,
+                          self.head_dim, _DT[self.dtype])
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH_DT[self.dtype]
+
+    @property
+    def pool_shape(self) -> tuple:
+        return (self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
+
+    @property
+    def state_numel(self) -> int:
+        return 16 + 2 * self.n_pages + self.n_slots * (1 + self.max_pages)
+
+
+def pages_state_bytes(pages: PageSpec) -> int:
+    n = ctypes.c_size_t()
+    capi.check("anchorkv_pages_state_bytes",
+               capi.lib().anchorkv_pages_state_bytes(ctypes.byref(pages.c()), ctypes.byref(n)))
+    return n.value
+
+
+def pages_workspace_bytes(pages: PageSpec) -> int:
+    """Scratch of pages_commit, pages_fork and pages_compact."""
+    n = ctypes.c_size_t()
+    capi.check("anchorkv_pages_workspace_bytes",
+               capi.lib().anchorkv_pages_workspace_bytes(ctypes.byref(pages.c()), ctypes.byref(n)))
+    return n.value
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def pages_init(pages: PageSpec, device="cuda", state: torch.Tensor | None = None) -> torch.Tensor:
+    """A page state (int32) in which every page is free and every slot empty."""
+    if state is None:
+        state = torch.empty(pages_state_bytes(pages) // 4, dtype=torch.int32, device=device)
+    _check_tensor("state", state, (pages.state_numel,), torch.int32)
+    with torch.cuda.device(state.device):
+        st = capi.lib().anchorkv_pages_init(ctypes.byref(pages.c()), _ptr(state), _stream(state.device))
+    capi.check("anchorkv_pages_init", st)
+    return state
+
+
+def pages_view(pages: PageSpec, state: torch.Tensor) -> dict:
+    """Views into a page state: status, n_free, free, refs, len, table."""
+    n, s, at = pages.n_pages, pages.n_slots, 16
+    return {"status": state[0], "n_free": state[1], "free": state[at:at + n], "refs": state[at + n:at + 2 * n],
+            "len": state[at + 2 * n:at + 2 * n + s], "table": state[at + 2 * n + s:].view(s, pages.max_pages)}
+
+
+def _pages_check(pages, state, K_pages, V_pages, state_out, workspace):
+    _check_tensor("state", state, (pages.state_numel,), torch.int32)
+    _check_tensor("K_pages", K_pages, pages.pool_shape, pages.torch_dtype)
+    _check_tensor("V_pages", V_pages, pages.pool_shape, pages.torch_dtype)
+    if state_out is None:
+        state_out = state
+    _check_tensor("state_out", state_out, (pages.state_numel,), torch.int32)
+    if workspace is None:
+        workspace = torch.empty(pages_workspace_bytes(pages), dtype=torch.uint8, device=state.device)
+    _same_device(state.device, K_pages=K_pages, V_pages=V_pages, state_out=state_out, workspace=workspace)
+    return state_out, workspace
+
+
+def pages_commit(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
+                 K_new: torch.Tensor, V_new: torch.Tensor, n_accept: torch.Tensor, path: torch.Tensor | None = None,
+                 state_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Append rows path[b, :n_accept[b]] (path None: 0, 1, ...) of the drafts
+    K_new, V_new [n_layers, batch, n_draft, H, D] to slot b, in every layer.
+    n_accept: int32 [batch]; path: int32 [batch, n_draft].  Updates the state
+    in place unless state_out is given; returns the new state.  Whether the
+    operation was possible is in the state's status word (read_status)."""
+    state_out, workspace = _pages_check(pages, state, K_pages, V_pages, state_out, workspace)
+    if K_new.dim() != 5:
+        raise ValueError(f"K_new: expected [n_layers, batch, n_draft, H, D], got {tuple(K_new.shape)}")
+    batch, drafts = K_new.shape[1:3]
+    shape = (pages.n_layers, batch, drafts, pages.n_kv_heads, pages.head_dim)
+    _check_tensor("K_new", K_new, shape, pages.torch_dtype)
+    _check_tensor("V_new", V_new, shape, pages.torch_dtype)
+    _check_tensor("n_accept", n_accept, (batch,), torch.int32)
+    if path is not None:
+        _check_tensor("path", path, (batch, drafts), torch.int32)
+    _same_device(state.device, K_new=K_new, V_new=V_new, n_accept=n_accept, path=path)
+    with torch.cuda.device(state.device):
+        st = capi.lib().anchorkv_pages_commit(ctypes.byref(pages.c()), _ptr(state), _ptr(state_out), _ptr(K_pages),
+                                              _ptr(V_pages), _ptr(K_new), _ptr(V_new), batch, drafts, _ptr(path),
+                                              _ptr(n_accept), _ptr(workspace), workspace.numel(),
+                                              _stream(state.device))
+    capi.check("anchorkv_pages_commit", st)
+    return state_out
+
+
+def pages_fork(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
+               parents: torch.Tensor, state_out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Slot s becomes a copy of what slot parents[s] (int32 [n_slots]) was; -1
+    empties it.  Full pages are shared, a partly filled last page is copied
+    for all copies but the first.  Returns the new state."""
+    state_out, workspace = _pages_check(pages, state, K_pages, V_pages, state_out, workspace)
+    _check_tensor("parents", parents, (pages.n_slots,), torch.int32)
+    _same_device(state.device, parents=parents)
+    with torch.cuda.device(state.device):
+        st = capi.lib().anchorkv_pages_fork(ctypes.byref(pages.c()), _ptr(state), _ptr(state_out), _ptr(K_pages),
+                                            _ptr(V_pages), _ptr(parents), _ptr(workspace), workspace.numel(),
+                                            _stream(state.device))
+    capi.check("anchorkv_pages_fork", st)
+    return state_out
+
+
+def pages_compact(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
+                  state_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Move the pages in use to the front of the pool.  Returns the new state."""
+    state_out, workspace = _pages_check(pages, state, K_pages, V_pages, state_out, workspace)
+    with torch.cuda.device(state.device):
+        st = capi.lib().anchorkv_pages_compact(ctypes.byref(pages.c()), _ptr(state), _ptr(state_out), _ptr(K_pages),
+                                               _ptr(V_pages), _ptr(workspace), workspace.numel(),
+                                               _stream(state.device))
+    capi.check("anchorkv_pages_compact", st)
+    return state_out
+
+
+def tree_workspace_bytes(p: AnchorKVParams, batch: int, drafts: int, pages: PageSpec | None = None) -> int:
+    n = ctypes.c_size_t()
+    pg = ctypes.byref(pages.c()) if pages is not None else None
+    capi.check("anchorkv_tree_workspace_bytes",
+               capi.lib().anchorkv_tree_workspace_bytes(ctypes.byref(p.c()), batch, drafts, pg, ctypes.byref(n)))
+    return n.value
+
+
+def _row_strides(name, t, shape, dtype):
+    """(sequence, token) strides of a [batch, T, heads, D] tensor whose heads
+    are contiguous; a dimension of one element has no stride to speak of."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    batch, drafts, heads, D = shape
+    if t.stride(3) != 1 or (heads > 1 and t.stride(2) != D):
+        raise ValueError(f"{name}: heads must be contiguous, got strides {t.stride()}")
+    tok = t.stride(1) if drafts > 1 else heads * D
+    return t.stride(0) if batch > 1 else drafts * tok, tok
+
+
+def tree_attn(p: AnchorKVParams, compressed: torch.Tensor | None, q: torch.Tensor, K_new: torch.Tensor,
+              V_new: torch.Tensor, n_new: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+              layout_of: torch.Tensor | None = None, pages: PageSpec | None = None, state: torch.Tensor | None = None,
+              K_pages: torch.Tensor | None = None, V_pages: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention for a tree of drafted tokens (anchorkv_tree_attn).
+    q: [batch, T, H_q, D] and K_new, V_new: [batch, T, H, D] of the drafts, T <= 64
+    (sequence and token strides are free, e.g. slices of a fused projection);
+    compressed: uint8 [n_layouts, stride] or [total_bytes], or None;
+    layout_of: int32 [batch], the layout of each sequence (default: b);
+    n_new: int32 [batch], drafts of each sequence (default T); mask: int64
+    [batch, T], bit i of mask[b, t] = draft t sees draft i (default: a chain);
+    pages, state, K_pages, V_pages: one layer's slice [n_pages, H, page_size, D]
+    of the pools with the exact tokens, slot b = sequence b.
+    Returns [batch, T, H_q, D] of p.dtype; rows t >= n_new[b] of `out` stay as
+    they are (zero when out is not given)."""
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [batch, n_draft, H_q, D], got {tuple(q.shape)}")
+    batch, drafts = q.shape[:2]
+    H, Hq, D, dt, dev = p.n_kv_heads, p.n_q_heads, p.head_dim, p.torch_dtype, q.device
+    t = capi.Tree(batch=batch, n_draft=drafts)
+    t.q_seq_stride, t.q_tok_stride = _row_strides("q", q, (batch, drafts, Hq, D), dt)
+    t.new_seq_stride, t.new_tok_stride = _row_strides("K_new", K_new, (batch, drafts, H, D), dt)
+    if _row_strides("V_new", V_new, (batch, drafts, H, D), dt) != (t.new_seq_stride, t.new_tok_stride):
+        raise ValueError(f"K_new and V_new: unequal strides {K_new.stride()} and {V_new.stride()}")
+    if compressed is not None:
+        if compressed.device.type != "cuda" or compressed.dtype != torch.uint8 or not compressed.is_contiguous():
+            raise ValueError("compressed must be a contiguous CUDA uint8 tensor")
+        if compressed.dim() == 1:
+            t.n_layouts, t.seq_stride_bytes = 1, (compressed.numel() + 15) // 16 * 16
+        else:
+            t.n_layouts, t.seq_stride_bytes = compressed.shape
+        if compressed.shape[-1] < anchorkv_bytes(p)["total_bytes"]:
+            raise ValueError(f"compressed: {compressed.shape[-1]} bytes are less than a layout")
+        t.compressed = compressed.data_ptr()
+    if layout_of is not None:
+        _check_tensor("layout_of", layout_of, (batch,), torch.int32)
+        t.layout_of = layout_of.data_ptr()
+    if n_new is not None:
+        _check_tensor("n_new", n_new, (batch,), torch.int32)
+        t.n_new = n_new.data_ptr()
+    if mask is not None:
+        _check_tensor("mask", mask, (batch, drafts), torch.int64)
+        t.mask = mask.data_ptr()
+    if pages is not None:
+        if state is None or K_pages is None or V_pages is None:
+            raise ValueError("pages need state, K_pages and V_pages")
+        _check_tensor("state", state, (pages.state_numel,), torch.int32)
+        _check_tensor("K_pages", K_pages, pages.pool_shape[1:], dt)
+        _check_tensor("V_pages", V_pages, pages.pool_shape[1:], dt)
+        pg = pages.c()
+        t.pages = ctypes.pointer(pg)
+        t.state, t.K_pages, t.V_pages = state.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr()
+    if out is None:
+        out = torch.zeros(batch, drafts, Hq, D, dtype=dt, device=dev)
+    _check_tensor("out", out, (batch, drafts, Hq, D), dt)
+    if workspace is None:
+        workspace = torch.empty(tree_workspace_bytes(p, batch, drafts, pages), dtype=torch.uint8, device=dev)
+    _same_device(dev, compressed=compressed, K_new=K_new, V_new=V_new, n_new=n_new, mask=mask, layout_of=layout_of,
+                 state=state, K_pages=K_pages, V_pages=V_pages, out=out, workspace=workspace)
+    t.q, t.K_new, t.V_new, t.out = q.data_ptr(), K_new.data_ptr(), V_new.data_ptr(), out.data_ptr()
+    with torch.cuda.device(dev):
+        st = capi.lib().anchorkv_tree_attn(ctypes.byref(p.c()), ctypes.byref(t), _ptr(workspace), workspace.numel(),
+                                           _stream(dev))
+    capi.check("anchorkv_tree_attn", st)
+    return out
+
+
 def reconstruct(p: AnchorKVParams, compressed: torch.Tensor):
     """Dense fp32 K^, V^ [H, N, D] of one compressed layer (inspection hook)."""
     H, N, D = p.n_kv_heads, p.n_tokens, p.head_dim
@@ -323,7 +552,7 @@ class HostCompressor:
         return compress_host(self.p, K_host, V_host, Q_host, dst, self.staging, self.ws, device=self.device)
 
 
-N_STAGES = 16   # ANCHORKV_N_STAGES
+N_STAGES = 18   # ANCHORKV_N_STAGES
 
 
 def stage_timing(enable: bool) -> None:

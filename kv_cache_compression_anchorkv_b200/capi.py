@@ -43,6 +43,25 @@ class WorkspaceView(ctypes.Structure):
                 ("off_assign_probe", ctypes.c_int64)]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_slots", "max_pages", "n_layers",
+                                              "n_kv_heads", "head_dim", "dtype")]
+
+
+class Tree(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("n_draft", ctypes.c_int32),
+        ("compressed", ctypes.c_void_p), ("seq_stride_bytes", ctypes.c_int64), ("n_layouts", ctypes.c_int32),
+        ("layout_of", ctypes.c_void_p),
+        ("q", ctypes.c_void_p), ("q_seq_stride", ctypes.c_int64), ("q_tok_stride", ctypes.c_int64),
+        ("K_new", ctypes.c_void_p), ("V_new", ctypes.c_void_p),
+        ("new_seq_stride", ctypes.c_int64), ("new_tok_stride", ctypes.c_int64),
+        ("n_new", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+        ("pages", ctypes.POINTER(Pages)), ("state", ctypes.c_void_p),
+        ("K_pages", ctypes.c_void_p), ("V_pages", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.POINTER
 _vp = ctypes.c_void_p
 _SIGS = {
@@ -63,6 +82,16 @@ _SIGS = {
     "anchorkv_decode_attn_rope": ([_P(Params), _vp, ctypes.c_int64, ctypes.c_int32, _vp, _vp, _vp, ctypes.c_int32,
                                    ctypes.c_int32, ctypes.c_double, _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
     "anchorkv_reconstruct": ([_P(Params), _vp, _vp, _vp, _vp], ctypes.c_int),
+    "anchorkv_pages_state_bytes": ([_P(Pages), _P(ctypes.c_size_t)], ctypes.c_int),
+    "anchorkv_pages_workspace_bytes": ([_P(Pages), _P(ctypes.c_size_t)], ctypes.c_int),
+    "anchorkv_pages_init": ([_P(Pages), _vp, _vp], ctypes.c_int),
+    "anchorkv_pages_commit": ([_P(Pages), _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int32, ctypes.c_int32, _vp, _vp, _vp,
+                               ctypes.c_size_t, _vp], ctypes.c_int),
+    "anchorkv_pages_fork": ([_P(Pages), _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+    "anchorkv_pages_compact": ([_P(Pages), _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+    "anchorkv_tree_workspace_bytes": ([_P(Params), ctypes.c_int32, ctypes.c_int32, _P(Pages), _P(ctypes.c_size_t)],
+                                      ctypes.c_int),
+    "anchorkv_tree_attn": ([_P(Params), _P(Tree), _vp, ctypes.c_size_t, _vp], ctypes.c_int),
     "anchorkv_read_device_status": ([_vp, _P(ctypes.c_int32), _vp], ctypes.c_int),
     "anchorkv_codebook": ([_P(ctypes.c_double)], ctypes.c_int),
     "anchorkv_strerror": ([ctypes.c_int], ctypes.c_char_p),

@@ -208,7 +208,7 @@ static bool use_tc_obs(const Plan& pl) {
   return obs_tc_supported(pl);
 }
 
-static int check_device() {
+int check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ANCHORKV_ECUDA;
   int major = 0;

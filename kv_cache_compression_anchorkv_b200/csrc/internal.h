@@ -12,8 +12,10 @@ namespace akv {
 enum Stage {
   kStObsPass1 = 0, kStObsCombine, kStTokenStats, kStAnchorSelect, kStAssign, kStRefine, kStProject,
   kStSelect, kStQuantize, kStDecodePrep, kStDecodeSplit, kStDecodeCombine, kStObsAlpha, kStObsKu, kStDecodeCluster,
-  kStDecodeRope, kStageCount
+  kStDecodeRope, kStPages, kStTree, kStageCount
 };
+// ANCHORKV_OK on an sm_100 device.
+int check_device();
 void stage_begin(int stage, cudaStream_t s);
 void stage_end(int stage, cudaStream_t s, int kernels);
 
@@ -121,6 +123,8 @@ inline int naive_codec(const Plan& pl) { return (pl.p.mode & ANCHORKV_MODE_NAIVE
 int launch_decode(const Plan& pl, const DecodePlan& dp, const char* comp, int64_t stride,
                   const void* q, const void* Kt, const void* Vt, int tail_len, int tail_cap,
                   float* out, char* ws, cudaStream_t s);
+// Tokens that the page tables of one sequence can hold (checks the sizes).
+int pages_tokens(const anchorkv_pages* pg, int64_t* most);
 cudaError_t launch_reconstruct(const Plan& pl, const char* comp, float* Kh, float* Vh, cudaStream_t s);
 
 }  // namespace akv

@@ -1,0 +1,76 @@
+// Plan and kernel arguments of the tree attention (tree_attn.cu and the
+// kernels it launches).
+#pragma once
+
+#include "internal.h"
+
+namespace akv {
+
+// Drafts of one sequence: bits of a mask word.
+constexpr int kTreeMaxDrafts = 64;
+
+// One call's shape: the rows (draft t, query head g) of a KV head, r = t G + g,
+// are cut into blocks of RB; every (sequence, head, block) is a unit, whose
+// tokens `parts` CTAs share.
+struct TreePlan {
+  int batch, T, rows, RB, n_blk, parts;
+  int64_t cap;                       // exact tokens that the page tables can hold
+  // workspace (bytes): status words, (max, sum) and outputs of every part
+  int64_t o_ml, o_part, ws_total;
+};
+
+struct TreeArgs {
+  const uint8_t* comp;               // null: no compressed tokens
+  int64_t stride;
+  int64_t off_ak, off_av, off_tok, off_bm, off_pf, off_codes, off_sig;
+  int n_layouts;
+  const int* layout_of;
+  int N, H, G, k, n_tiles;
+  int64_t R;
+  float lev[4];
+  uint32_t sign_bits[4];
+  int naive;
+  int batch, T, RB, n_blk, parts;
+  const void* q;
+  int64_t q_seq, q_tok;
+  const void* kn;
+  const void* vn;
+  int64_t n_seq, n_tok;
+  const int* n_new;
+  const unsigned long long* mask;
+  // pages (table null: none)
+  const int* len;
+  const int* table;
+  int n_pages, P, maxp;
+  const void* kp;
+  const void* vp;
+  void* out;
+  int* counters;
+  float* ml;                         // [unit][part][RB] (max, sum)
+  float* part;                       // [unit][part][RB][D]
+};
+
+// Drafts of sequence b.
+__device__ __forceinline__ int tree_new(const TreeArgs& a, int b) {
+  const int n = a.n_new ? a.n_new[b] : a.T;
+  return n < 0 ? 0 : (n > a.T ? a.T : n);
+}
+// Layout of sequence b; -1 where layout_of is out of its range.
+__device__ __forceinline__ int tree_layout(const TreeArgs& a, int b) {
+  const int l = a.layout_of ? a.layout_of[b] : b;
+  return l < 0 || l >= a.n_layouts ? -1 : l;
+}
+// Exact tokens of sequence b; -1 where the state's length is out of its range.
+__device__ __forceinline__ int tree_len(const TreeArgs& a, int b) {
+  if (!a.table) return 0;
+  const int n = a.len[b];
+  return n < 0 || n > (int64_t)a.maxp * a.P ? -1 : n;
+}
+__device__ __forceinline__ unsigned long long tree_mask(const TreeArgs& a, int b, int t) {
+  return a.mask ? a.mask[(int64_t)b * a.T + t] : (2ull << t) - 1;
+}
+
+void tree_plan_simt(const Plan& pl, TreePlan* tp);
+int launch_tree_simt(const Plan& pl, const TreeArgs& a, cudaStream_t s);
+
+}  // namespace akv
