@@ -14,9 +14,11 @@ constexpr int kTreeMaxDrafts = 64;
 // tokens `parts` CTAs share.
 struct TreePlan {
   int batch, T, rows, RB, n_blk, parts;
+  int tail_parts;                    // of those, CTAs of exact tokens only (tensor-core kernel)
   int64_t cap;                       // exact tokens that the page tables can hold
-  // workspace (bytes): status words, (max, sum) and outputs of every part
-  int64_t o_ml, o_part, ws_total;
+  // workspace (bytes): status words, (max, sum) and outputs of every
+  // part; tensor-core kernel: rotated anchors, their scales, infinite values
+  int64_t o_ml, o_part, o_anc, o_anc_scale, o_inf, ws_total;
 };
 
 struct TreeArgs {
@@ -30,7 +32,7 @@ struct TreeArgs {
   float lev[4];
   uint32_t sign_bits[4];
   int naive;
-  int batch, T, RB, n_blk, parts;
+  int batch, T, RB, n_blk, parts, tail_parts;
   const void* q;
   int64_t q_seq, q_tok;
   const void* kn;
@@ -48,6 +50,9 @@ struct TreeArgs {
   int* counters;
   float* ml;                         // [unit][part][RB] (max, sum)
   float* part;                       // [unit][part][RB][D]
+  void* anc;                         // [batch][2][H][k][D] fp16, rotated
+  float* anc_scale;                  // [batch][2][H][k]
+  unsigned long long* inf_v;         // [batch][H] drafts with an infinite or NaN value
 };
 
 // Drafts of sequence b.
@@ -70,7 +75,9 @@ __device__ __forceinline__ unsigned long long tree_mask(const TreeArgs& a, int b
   return a.mask ? a.mask[(int64_t)b * a.T + t] : (2ull << t) - 1;
 }
 
+void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp);
+int launch_tree_tc(const TreeArgs& a, cudaStream_t s);
 void tree_plan_simt(const Plan& pl, TreePlan* tp);
-int launch_tree_simt(const Plan& pl, const TreeArgs& a, cudaStream_t s);
+int launch_tree_simt(const TreeArgs& a, cudaStream_t s);
 
 }  // namespace akv

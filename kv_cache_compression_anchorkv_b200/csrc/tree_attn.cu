@@ -7,7 +7,8 @@
 namespace akv {
 namespace {
 
-int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pages* pg, Plan* pl, TreePlan* tp) {
+int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pages* pg, bool prefix, Plan* pl,
+                   TreePlan* tp) {
   int st = make_plan(p, pl);
   if (st) return st;
   if (batch < 0 || T < 1 || T > kTreeMaxDrafts) return ANCHORKV_EINVAL;
@@ -22,12 +23,21 @@ int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pa
     if (pg->n_kv_heads != pl->H || pg->dtype != p->dtype || batch > pg->n_slots) return ANCHORKV_EINVAL;
     if (tp->cap > (1 << 20)) return ANCHORKV_EUNSUPPORTED;
   }
-  tree_plan_simt(*pl, tp);
+  // bf16 caches on the tensor cores; fp32 caches need 32-bit products
+  const bool tcore = p->dtype == ANCHORKV_BF16;
+  if (tcore) tree_plan_tc(*pl, prefix, tp);
+  else tree_plan_simt(*pl, tp);
   const int64_t parts = (int64_t)tp->batch * pl->H * tp->n_blk * tp->parts * tp->RB;
   int64_t off = 256;                                                     // status words
   auto take = [&](int64_t bytes) { const int64_t o = off; off += (bytes + 255) / 256 * 256; return o; };
   tp->o_ml = take(8 * parts);
   tp->o_part = take(4 * kD * parts);
+  if (tcore) {
+    const int64_t rows = (int64_t)tp->batch * 2 * pl->H * pl->k;
+    tp->o_anc = take(2 * kD * rows);
+    tp->o_anc_scale = take(4 * rows);
+    tp->o_inf = take(8 * (int64_t)tp->batch * pl->H);
+  }
   tp->ws_total = off;
   return ANCHORKV_OK;
 }
@@ -44,9 +54,14 @@ int anchorkv_tree_workspace_bytes(const anchorkv_params* p, int32_t batch, int32
   if (!ws_bytes) return ANCHORKV_EINVAL;
   Plan pl;
   TreePlan tp;
-  const int st = make_tree_plan(p, batch, n_draft, pg, &pl, &tp);
-  if (st) return st;
-  *ws_bytes = (size_t)tp.ws_total;
+  // the split differs with and without compressed tokens
+  int64_t most = 0;
+  for (const bool prefix : {true, false}) {
+    const int st = make_tree_plan(p, batch, n_draft, pg, prefix, &pl, &tp);
+    if (st) return st;
+    most = std::max(most, tp.ws_total);
+  }
+  *ws_bytes = (size_t)most;
   return ANCHORKV_OK;
 }
 
@@ -54,7 +69,7 @@ int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* w
   if (!t) return ANCHORKV_EINVAL;
   Plan pl;
   TreePlan tp;
-  int st = make_tree_plan(p, t->batch, t->n_draft, t->pages, &pl, &tp);
+  int st = make_tree_plan(p, t->batch, t->n_draft, t->pages, t->compressed != nullptr, &pl, &tp);
   if (st) return st;
   if (t->batch == 0) return ANCHORKV_OK;
   if (!t->q || !t->K_new || !t->V_new || !t->out || !ws) return ANCHORKV_EINVAL;
@@ -91,6 +106,7 @@ int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* w
   for (int i = 0; i < 4; ++i) a.sign_bits[i] = pl.sign_bits[i];
   a.naive = naive_codec(pl);
   a.batch = t->batch; a.T = t->n_draft; a.RB = tp.RB; a.n_blk = tp.n_blk; a.parts = tp.parts;
+  a.tail_parts = tp.tail_parts;
   a.q = t->q; a.q_seq = t->q_seq_stride; a.q_tok = t->q_tok_stride;
   a.kn = t->K_new; a.vn = t->V_new; a.n_seq = t->new_seq_stride; a.n_tok = t->new_tok_stride;
   a.n_new = t->n_new;
@@ -108,10 +124,12 @@ int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* w
   a.ml = (float*)(w + tp.o_ml);
   a.part = (float*)(w + tp.o_part);
   cudaStream_t s = (cudaStream_t)stream;
+  a.anc = w + tp.o_anc;
+  a.anc_scale = (float*)(w + tp.o_anc_scale);
+  a.inf_v = (unsigned long long*)(w + tp.o_inf);
   stage_begin(kStTree, s);
-  if (cudaMemsetAsync(w, 0, 64, s) != cudaSuccess) return ANCHORKV_ECUDA;
-  st = launch_tree_simt(pl, a, s);
-  stage_end(kStTree, s, 2);
+  st = p->dtype == ANCHORKV_BF16 ? launch_tree_tc(a, s) : launch_tree_simt(a, s);
+  stage_end(kStTree, s, p->dtype == ANCHORKV_BF16 ? 3 : 2);
   return st;
 }
 

@@ -1,4 +1,4 @@
-// Tree attention over compressed caches in fp32.
+// Tree attention over fp32 compressed caches.
 //
 // "AnchorKV: Anchor-Residual KV Cache Compression" (pith.science review),
 // Referee "Summary": a FlashAttention-style decoder rebuilds tiles when they
@@ -38,13 +38,12 @@ struct Sm {
 };
 
 // One token of the prefix, four coordinates per lane.
-template <typename T>
 __device__ __forceinline__ void rebuild(const TreeArgs& a, const uint8_t* comp, int side, int h, int t, float (&x)[4]) {
   const int lane = threadIdx.x & 31;
   const uint32_t w = reinterpret_cast<const uint32_t*>(comp + a.off_tok)[((int64_t)side * a.H + h) * a.N + t];
   const int slot = min((int)(w & 0xffffu), a.k - 1);
-  const T* anc = reinterpret_cast<const T*>(comp + (side ? a.off_av : a.off_ak)) + ((int64_t)h * a.k + slot) * kD;
-  load4<T>(anc + lane * 4, x);
+  const float* anc = reinterpret_cast<const float*>(comp + (side ? a.off_av : a.off_ak)) + ((int64_t)h * a.k + slot) * kD;
+  load4<float>(anc + lane * 4, x);
   const float gm = half_bits_to_f(w >> 16);
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] *= gm;
@@ -78,7 +77,6 @@ __device__ __forceinline__ void rebuild(const TreeArgs& a, const uint8_t* comp, 
   for (int i = 0; i < 4; ++i) x[i] += z[i];
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kThr) tree_simt_kernel(TreeArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>(raw);
@@ -100,7 +98,7 @@ __global__ void __launch_bounds__(kThr) tree_simt_kernel(TreeArgs a) {
     const int r = blk * kRB + i / kD, d = i % kD;
     float v = 0.f;
     if (r < rows)
-      v = to_f<T>(reinterpret_cast<const T*>(a.q)[b * a.q_seq + (r / a.G) * a.q_tok + (h * a.G + r % a.G) * kD + d]) * qs;
+      v = reinterpret_cast<const float*>(a.q)[b * a.q_seq + (r / a.G) * a.q_tok + (h * a.G + r % a.G) * kD + d] * qs;
     sm.q[i / kD][d] = v;
   }
   if (tid < kRB) {
@@ -124,21 +122,21 @@ __global__ void __launch_bounds__(kThr) tree_simt_kernel(TreeArgs a) {
       const int t = tt + j;
       if (j < nt) {
         if (t < n_pre) {
-          rebuild<T>(a, comp, 0, h, t, k4);
-          rebuild<T>(a, comp, 1, h, t, v4);
+          rebuild(a, comp, 0, h, t, k4);
+          rebuild(a, comp, 1, h, t, v4);
         } else if (t < n_pre + len) {
           const int u = t - n_pre, pg = a.table[(int64_t)b * a.maxp + u / a.P];
           if (pg >= 0 && pg < a.n_pages) {
             const int64_t at = (((int64_t)pg * a.H + h) * a.P + u % a.P) * kD + lane * 4;
-            load4<T>(reinterpret_cast<const T*>(a.kp) + at, k4);
-            load4<T>(reinterpret_cast<const T*>(a.vp) + at, v4);
+            load4<float>(reinterpret_cast<const float*>(a.kp) + at, k4);
+            load4<float>(reinterpret_cast<const float*>(a.vp) + at, v4);
           } else if (lane == 0) {
             bad_page = 1;
           }
         } else {
           const int64_t at = b * a.n_seq + (int64_t)(t - n_pre - len) * a.n_tok + h * kD + lane * 4;
-          load4<T>(reinterpret_cast<const T*>(a.kn) + at, k4);
-          load4<T>(reinterpret_cast<const T*>(a.vn) + at, v4);
+          load4<float>(reinterpret_cast<const float*>(a.kn) + at, k4);
+          load4<float>(reinterpret_cast<const float*>(a.vn) + at, v4);
         }
       }
       *reinterpret_cast<float4*>(&sm.K[j][lane * 4]) = make_float4(k4[0], k4[1], k4[2], k4[3]);
@@ -214,7 +212,6 @@ __global__ void __launch_bounds__(kThr) tree_simt_kernel(TreeArgs a) {
 }
 
 // One warp per output row: the parts joined by their maxima and sums.
-template <typename T>
 __global__ void __launch_bounds__(kThr) tree_simt_merge_kernel(TreeArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kThr / 32) + (threadIdx.x >> 5);
@@ -241,31 +238,8 @@ __global__ void __launch_bounds__(kThr) tree_simt_merge_kernel(TreeArgs a) {
     x[3] = fmaf(w, v.w, x[3]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* out = reinterpret_cast<T*>(a.out) + i * kD + lane * 4;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] = (T)(x[e] * inv);   // the one rounding to the output's type
-}
-
-template <typename T>
-int launch_t(const TreeArgs& a, cudaStream_t s) {
-  static std::mutex mu;
-  static int ready_dev = -1;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ANCHORKV_ECUDA;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (ready_dev != dev) {
-      if (cudaFuncSetAttribute(tree_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Sm)) !=
-          cudaSuccess)
-        return ANCHORKV_ECUDA;
-      ready_dev = dev;
-    }
-  }
-  tree_simt_kernel<T><<<dim3(a.parts, a.n_blk, a.batch * a.H), kThr, sizeof(Sm), s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
-  tree_simt_merge_kernel<T><<<(unsigned)((rows + kThr / 32 - 1) / (kThr / 32)), kThr, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ANCHORKV_OK : ANCHORKV_ECUDA;
+  float* out = reinterpret_cast<float*>(a.out) + i * kD + lane * 4;
+  *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
 }
 
 }  // namespace
@@ -278,8 +252,26 @@ void tree_plan_simt(const Plan& pl, TreePlan* tp) {
   tp->parts = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (2 * 148 + units - 1) / units));
 }
 
-int launch_tree_simt(const Plan& pl, const TreeArgs& a, cudaStream_t s) {
-  return pl.p.dtype == ANCHORKV_BF16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<float>(a, s);
+int launch_tree_simt(const TreeArgs& a, cudaStream_t s) {
+  static std::mutex mu;
+  static int ready_dev = -1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ANCHORKV_ECUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (ready_dev != dev) {
+      if (cudaFuncSetAttribute(tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Sm)) !=
+          cudaSuccess)
+        return ANCHORKV_ECUDA;
+      ready_dev = dev;
+    }
+  }
+  if (cudaMemsetAsync(a.counters, 0, 64, s) != cudaSuccess) return ANCHORKV_ECUDA;
+  tree_simt_kernel<<<dim3(a.parts, a.n_blk, a.batch * a.H), kThr, sizeof(Sm), s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
+  const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
+  tree_simt_merge_kernel<<<(unsigned)((rows + kThr / 32 - 1) / (kThr / 32)), kThr, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ANCHORKV_OK : ANCHORKV_ECUDA;
 }
 
 }  // namespace akv
