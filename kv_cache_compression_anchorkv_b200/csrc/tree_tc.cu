@@ -60,7 +60,9 @@ constexpr int kHalf = kTileBytes / 2;     // 64 coordinates of every row
 constexpr int kOCols = 64;                // output columns in tensor memory
 constexpr int kTmemCols = 256;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPTarget = 10.f;          // a new reference puts the largest |w p| at 2^9 .. 2^10
+// A new reference puts the largest |w p| between 1/2 and 1: 2^15 above it for
+// later tiles, and what fp16 rounds away below 2^-14 is at most 2^-25 of the
+// largest contribution each.
 constexpr float kPLimit = 32768.f;        // fp16 holds 65504
 constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
 constexpr float kRefGap = 120.f;          // the references' largest distance downwards
@@ -77,7 +79,7 @@ struct Sm {
   int idx[2][2][kTT];                     // anchor slots, [side][tile parity]
   float cs[64], nm[64], cw[64], mp[64];   // per row: logit scale, -reference of the sum, 2^(sum's - w p's), w p's
   float fl[64], fp[64];                   // rescaling factors
-  float red[2][4][32];
+  int red[2][4][32];
   float lsum[4][64];
   unsigned long long mask[kTreeMaxDrafts];
   unsigned char colt[64];                 // draft of each row
@@ -125,6 +127,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Floats as integers in the same order (its own inverse), for the warp-wide
+// integer maximum.
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 // Instruction descriptor of kind::f16 with fp16 operands and fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
@@ -627,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
               const int c = c0 + x + y;
               const bool seen = !special || ((vis >> sm.colt[c]) & 1ull);
               const float lg = seen ? __uint_as_float(s[y]) * (rk * sm.cs[c]) : -INFINITY;
-              const float m1 = warp_max(lg), m2 = warp_max(lg + lw);
+              const int m1 = __reduce_max_sync(0xffffffffu, ordered(lg));
+              const int m2 = __reduce_max_sync(0xffffffffu, ordered(lg + lw));
               if (lane == 0) {
                 sm.red[0][warp][x + y] = m1;
                 sm.red[1][warp][x + y] = m2;
@@ -637,11 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
           tc::named_bar(1, 128);
           if (tid < CW) {
             const int c = c0 + tid;
-            const float m1 = fmaxf(fmaxf(sm.red[0][0][tid], sm.red[0][1][tid]), fmaxf(sm.red[0][2][tid], sm.red[0][3][tid]));
-            const float m2 = fmaxf(fmaxf(sm.red[1][0][tid], sm.red[1][1][tid]), fmaxf(sm.red[1][2][tid], sm.red[1][3][tid]));
+            const float m1 = unordered(max(max(sm.red[0][0][tid], sm.red[0][1][tid]), max(sm.red[0][2][tid], sm.red[0][3][tid])));
+            const float m2 = unordered(max(max(sm.red[1][0][tid], sm.red[1][1][tid]), max(sm.red[1][2][tid], sm.red[1][3][tid])));
             const float l_old = -sm.nm[c], p_old = sm.mp[c];
             const float l_new = fmaxf(l_old, ceilf(m1));
-            float p_new = fmaxf(p_old, ceilf(m2) - kPTarget);
+            float p_new = fmaxf(p_old, ceilf(m2));
             if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
             sm.fl[c] = l_old > -INFINITY ? exp2f(l_old - l_new) : 0.f;
             sm.fp[c] = p_old > -INFINITY ? exp2f(p_old - p_new) : 0.f;
