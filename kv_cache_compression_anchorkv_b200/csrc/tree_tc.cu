@@ -28,12 +28,12 @@
 // Tokens are on the accumulator's lanes, so a thread owns a token: its scales
 // are scalars, its row of P is contiguous, and the cost of the softmax goes
 // with the rows there are (16, 32 or 64 columns) instead of a padded 128.
-//   warps 0-3   softmax: logits from tensor memory, exponentials, P to shared
-//               memory; at the end the outputs
-//   warps 4-7, 8-11  key and value tiles: anchor rows by 16-byte asynchronous
-//               copies into the 128-byte swizzle, residual rows finished in
-//               place (one half-warp each), one tile behind the copies
-//   warp 12     issues the MMAs
+//   softmax, 4 warps for 16 or 32 rows and 8 for 64: logits from tensor
+//     memory, exponentials, P to shared memory; at the end the outputs
+//   one warp issues the MMAs
+//   7 warps fill key and value tiles, 32 rows a job: anchor rows by 16-byte
+//     asynchronous copies into the 128-byte swizzle, residual rows finished in
+//     place (half a warp each), one job behind the copies
 // The maximum over tokens would need a reduction across lanes for every row
 // and tile.  Instead each row keeps two power-of-two references, one for the
 // sum of p and one for w p (the fp16 operand), which move only when a tile
@@ -52,7 +52,7 @@ namespace akv {
 namespace {
 
 constexpr int kTT = 128;                  // tokens of a tile
-constexpr int kThreads = 13 * 32;
+constexpr int kProd = 7;                  // producer warps
 constexpr int kKSt = 2, kVSt = 2;         // stages of the key and value rings
 constexpr int kKSl = kKSt + 2;            // key scales outlive their tile by the two logit buffers
 constexpr int kTileBytes = kTT * kD * 2;
@@ -72,18 +72,16 @@ struct Sm {
   uint8_t V[kVSt][kTileBytes];
   uint8_t P[2][kTT * 128];                // [token][64 rows] fp16, swizzled
   uint8_t Q[64 * kD * 2];
-  uint8_t codes[2][2][kTT * kCodeBytes];  // [side][tile parity]
-  int4 ent[2][3][kTT];                    // residual rows of a tile: row, anchor factor, level table
+  uint8_t codes[kProd][2][32 * kCodeBytes];   // of a producer's job and the one before
   float rk[kKSl][kTT];                    // key scales
   float wv[kVSt][kTT];                    // value scales
-  int idx[2][2][kTT];                     // anchor slots, [side][tile parity]
   float cs[64], nm[64], cw[64], mp[64];   // per row: logit scale, -reference of the sum, 2^(sum's - w p's), w p's
   float fl[64], fp[64];                   // rescaling factors
-  int red[2][4][32];
+  int red[2][4][64];
   float lsum[4][64];
   unsigned long long mask[kTreeMaxDrafts];
   unsigned char colt[64];                 // draft of each row
-  uint64_t kfull[kKSt], kempty[kKSt], vfull[kVSt], pv[2], sfull[2], sempty[2], pfull[2], sk[kKSl], sv[kVSt];
+  uint64_t full[2][2], kempty[kKSt], pv[2], sfull[2], sempty[2], pfull[2], sk[kKSl], sv[kVSt];   // full: [side][stage]
   uint32_t tmem;
   int err, bad, rep;
 };
@@ -190,166 +188,213 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   }
 }
 
-// What the producers of one side know of their CTA.
-struct Prod {
-  Sm* sm;
-  int side, tid, n;                       // thread in the group, tiles
-  uint8_t* ring;
-  uint64_t *full, *empty, *scales;
-  int stages, slots;
-};
-
+// Waits for a phase.  A phase that is over already, the usual case in a full
+// pipeline, costs one test; the bounded wait is out of the way of that path.
+__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, int* err, int* counters) {
+  if (*(volatile int*)err) return;
+  tc::wait_or_fail(bar, parity, err, counters, kDevErrTimeout);
+}
 __device__ __forceinline__ void wait_b(Sm& sm, uint64_t* bar, uint32_t parity, const TreeArgs& a) {
-  if (*(volatile int*)&sm.err) return;
-  tc::wait_or_fail(bar, parity, &sm.err, a.counters, kDevErrTimeout);
+  if (!tc::mbar_done(bar, parity)) wait_slow(bar, parity, &sm.err, a.counters);
 }
 
 __device__ __forceinline__ uint32_t swz(int row, int chunk) {   // byte offset of a row's 16-byte piece in a tile
   return (uint32_t)((chunk >> 3) * kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-// Token words of one tile, one token per thread: its word, its bitmap word,
-// and the record before the first of its word.
+// Work of a producer warp: 32 rows of one tile and side.  Jobs are numbered
+// tile by tile (four quarters of the keys, four of the values) and go round
+// the producer warps, which need nothing from one another.
+struct Job {
+  int tile, side, q;                      // tile of this CTA's share, quarter
+};
+__device__ __forceinline__ Job job_of(int id) { return Job{id >> 3, (id >> 2) & 1, id & 3}; }
+
+// The job's stage is free: the products that read its last tile are done
+// (keys: the logits, values: the outputs).
+__device__ __forceinline__ uint64_t* stage_free(Sm& sm, const Job& j) {
+  return j.side ? &sm.pv[j.tile & 1] : &sm.kempty[j.tile & 1];
+}
+
+__device__ __forceinline__ void job_scales(Sm& sm, const Job& j, int row, float w) {
+  (j.side ? sm.wv[j.tile % kVSt] : sm.rk[j.tile % kKSl])[row] = w;
+}
+__device__ __forceinline__ void job_scales_done(Sm& sm, const Job& j) {
+  tc::mbar_arrive(j.side ? &sm.sv[j.tile % kVSt] : &sm.sk[j.tile % kKSl]);
+}
+
+// What a job's 32 tokens are, one per lane, as loaded: token word, the tile's
+// bitmap and its first record.
+struct Raw {
+  uint32_t word;
+  uint4 bm;
+  int rec;
+};
+// ... and as used: the bitmap's word and the record of its first bit.
 struct Tok {
   uint32_t word, bits;
   int rec;
-  bool in;
 };
 
-__device__ __forceinline__ Tok load_tok(const TreeArgs& a, const uint8_t* comp, int sh, int tile, int i) {
-  Tok t;
-  const int64_t at = (int64_t)tile * kTT + i;
-  t.in = at < a.N;
-  t.word = t.in ? reinterpret_cast<const uint32_t*>(comp + a.off_tok)[(int64_t)sh * a.N + at] : 0u;
-  const uint4 w = *reinterpret_cast<const uint4*>(comp + a.off_bm + ((int64_t)sh * a.n_tiles + tile) * 16);
+__device__ __forceinline__ Raw load_tok(const TreeArgs& a, const uint8_t* comp, int h, int tile0, int n, int id) {
+  const Job j = job_of(id);
+  Raw t = {0u, make_uint4(0u, 0u, 0u, 0u), 0};
+  if (j.tile >= n) return t;
+  const int sh = j.side * a.H + h, tile = tile0 + j.tile;
+  const int at = tile * kTT + j.q * 32 + (threadIdx.x & 31);
+  if (at < a.N) t.word = reinterpret_cast<const uint32_t*>(comp + a.off_tok)[(int64_t)sh * a.N + at];
+  t.bm = *reinterpret_cast<const uint4*>(comp + a.off_bm + ((int64_t)sh * a.n_tiles + tile) * 16);
   t.rec = reinterpret_cast<const int*>(comp + a.off_pf)[(int64_t)sh * (a.n_tiles + 1) + tile];
-  const int q = i >> 5;
-  t.bits = q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w;
-  if (q > 0) t.rec += __popc(w.x);
-  if (q > 1) t.rec += __popc(w.y);
-  if (q > 2) t.rec += __popc(w.z);
-  if (!t.in) t.bits = 0u;                 // bits behind the last token mean nothing
   return t;
 }
 
-__device__ void produce_prefix(const TreeArgs& a, const Prod& p, const uint8_t* comp, int rep, int h, int tile0) {
-  Sm& sm = *p.sm;
-  const int i = p.tid, lane = i & 31, sh = p.side * a.H + h, bar_id = 2 + p.side;
-  const int64_t row0 = ((int64_t)rep * 2 * a.H + sh) * a.k;
-  const uint8_t* rows = reinterpret_cast<const uint8_t*>(a.anc) + row0 * (kD * 2);
-  const float* scale = a.anc_scale + row0;
+__device__ __forceinline__ Tok make_tok(const TreeArgs& a, const Raw& r, int tile0, int id) {
+  const Job j = job_of(id);
+  Tok t = {r.word, j.q == 0 ? r.bm.x : j.q == 1 ? r.bm.y : j.q == 2 ? r.bm.z : r.bm.w, r.rec};
+  if (j.q > 0) t.rec += __popc(r.bm.x);
+  if (j.q > 1) t.rec += __popc(r.bm.y);
+  if (j.q > 2) t.rec += __popc(r.bm.z);
+  const int left = a.N - ((tile0 + j.tile) * kTT + j.q * 32);          // bits behind the last token mean nothing
+  if (left < 32) t.bits &= left > 0 ? (1u << left) - 1u : 0u;
+  if (t.rec < 0 || t.rec + (int64_t)__popc(t.bits) > a.R) t.bits = 0u;
+  return t;
+}
+
+__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* comp, int rep, int h, int tile0) {
+  const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4;
+  const int64_t row0 = ((int64_t)rep * 2 * a.H + h) * a.k, side_rows = (int64_t)a.H * a.k;
   const uint8_t* codes = comp + a.off_codes;
   const uint16_t* sig = reinterpret_cast<const uint16_t*>(comp + a.off_sig);
-  const uint32_t ring = tc::smem_u32(p.ring);
-  // two tiles ahead the token words, one tile ahead what hangs on them
   auto slot_of = [&](const Tok& t) { return min((int)(t.word & 0xffffu), a.k - 1); };
-  auto rec_of = [&](const Tok& t) {
-    const int r = t.rec + __popc(t.bits & ((1u << lane) - 1u));
-    return (t.bits >> lane) & 1u && r >= 0 && r < a.R ? r : -1;
+  auto scale_of = [&](const Tok& t, int id) { return a.anc_scale[row0 + job_of(id).side * side_rows + slot_of(t)]; };
+  auto sigma_of = [&](const Tok& t) {
+    return (t.bits >> lane) & 1u ? half_bits_to_f(sig[t.rec + __popc(t.bits & ((1u << lane) - 1u))]) : 0.f;
   };
-  Tok t0 = load_tok(a, comp, sh, tile0, i);
-  Tok t1 = p.n > 1 ? load_tok(a, comp, sh, tile0 + 1, i) : t0;
-  float m0 = scale[slot_of(t0)];
-  float s0 = rec_of(t0) >= 0 ? half_bits_to_f(sig[rec_of(t0)]) : 0.f;
-  int n_rec_last = 0;
+  // Token words two jobs ahead, what hangs on them one job ahead.  Loaded words
+  // are first looked at a job later, so that no job waits for memory.
+  const Raw r0 = load_tok(a, comp, h, tile0, n, w);
+  Raw r1 = load_tok(a, comp, h, tile0, n, w + kProd);
+  Tok t0 = make_tok(a, r0, tile0, w);
+  float m0 = scale_of(t0, w), s0 = sigma_of(t0);
+  // the job whose copies are in flight: its residual rows, their factors
+  bool pending = false;
+  Job last = {};
+  uint32_t last_bits = 0, last_f = 0;
+  int parity = 0;
 
-  for (int j = 0; j <= p.n; ++j) {
-    int n_rec = 0;
-    if (j < p.n) {
-      const int st = j % p.stages, u = j / p.stages;
-      const Tok t = t0;
-      const float m = m0, sg = s0;
-      t0 = t1;
-      if (j + 2 < p.n) t1 = load_tok(a, comp, sh, tile0 + j + 2, i);
-      if (j + 1 < p.n) {
-        m0 = scale[slot_of(t0)];
-        const int r = rec_of(t0);
-        s0 = r >= 0 ? half_bits_to_f(sig[r]) : 0.f;
-      }
-      if (u > 0) wait_b(sm, &p.empty[st], (u - 1) & 1, a);
-      // scale of the row, and the residual's table
-      const int rec = rec_of(t);
-      const float c1 = half_bits_to_f(t.word >> 16) * m;
-      float w = c1;
-      int4 e = make_int4(i, 0, 0, 0);
-      if (rec >= 0) {
-        const bool by_anchor = fabsf(c1) >= sg;
-        w = by_anchor ? c1 : sg;
-        const float ca = by_anchor ? 1.f : c1 / sg, cb = by_anchor ? (c1 != 0.f ? sg / c1 : 0.f) : 1.f;
-        e.y = (int)pack_half2(ca, ca);
-        e.z = (int)pack_half2(cb * a.lev[0], cb * a.lev[1]);
-        e.w = (int)pack_half2(cb * a.lev[2], cb * a.lev[3]);
-      }
-      (p.side ? sm.wv : sm.rk)[j % p.slots][i] = t.in ? w : 0.f;
-      sm.idx[p.side][j & 1][i] = slot_of(t);
-      // this word's records follow those of the words before it
-      const uint4 bw = *reinterpret_cast<const uint4*>(comp + a.off_bm + ((int64_t)sh * a.n_tiles + tile0 + j) * 16);
-      const int first = reinterpret_cast<const int*>(comp + a.off_pf)[(int64_t)sh * (a.n_tiles + 1) + tile0 + j];
-      n_rec = __popc(bw.x) + __popc(bw.y) + __popc(bw.z) + __popc(bw.w);
-      if (first < 0 || first > a.R) n_rec = 0;
-      else n_rec = (int)min((int64_t)n_rec, a.R - first);
-      if (rec >= 0 && rec - first >= 0 && rec - first < kTT) sm.ent[p.side][j % 3][rec - first] = e;
-      tc::mbar_arrive(&p.scales[j % p.slots]);
-      tc::named_bar(bar_id, 128);
-      // rows: sixteen lanes each
-      const uint32_t base = ring + st * kTileBytes;
-      const int c = i & 15;
-#pragma unroll 4
-      for (int r = i >> 4; r < kTT; r += 8)
-        cp_async16(base + swz(r, c), rows + (int64_t)sm.idx[p.side][j & 1][r] * (kD * 2) + c * 16);
-      const uint32_t cd = tc::smem_u32(sm.codes[p.side][j & 1]);
-      for (int x = i; x < n_rec * 2; x += 128) cp_async16(cd + x * 16, codes + (int64_t)first * kCodeBytes + x * 16);
-      cp_commit();
-    }
-    if (j > 0) {
-      // the tile before: its copies have landed; finish its residual rows
-      const int st = (j - 1) % p.stages;
-      if (j < p.n) cp_wait<1>();
-      else cp_wait<0>();
-      tc::named_bar(bar_id, 128);
-      uint8_t* tile = p.ring + st * kTileBytes;
-      const uint8_t* cd = sm.codes[p.side][(j - 1) & 1];
-      const int c = i & 15;
-      for (int x = i >> 4; x < n_rec_last; x += 8) {
-        const int4 e = sm.ent[p.side][(j - 1) % 3][x];
-        const uint32_t code = *reinterpret_cast<const uint16_t*>(cd + x * kCodeBytes + c * 2);
-        uint4* at = reinterpret_cast<uint4*>(tile + swz(e.x & 127, c));
+  auto finish = [&](uint32_t buf) {
+    uint8_t* tile = last.side ? sm.V[last.tile & 1] : sm.K[last.tile & 1];
+    const uint8_t* cd = sm.codes[w][buf] + c * 2;
+    const __half l0 = __float2half_rn(a.lev[0]), l1 = __float2half_rn(a.lev[1]);
+    const __half2 lo = __halves2half2(l0, l1), hi = __halves2half2(__hneg(l1), __hneg(l0));
+    __syncwarp();                                          // the whole warp's copies have landed
+    int x = hw;
+    for (uint32_t m = last_bits; m; x += 2) {
+      const int b0 = __ffs(m) - 1;
+      m &= m - 1;
+      const int b1 = m ? __ffs(m) - 1 : -1;
+      m &= m - 1;
+      const int tk = hw ? b1 : b0;
+      const uint32_t f = __shfl_sync(0xffffffffu, last_f, max(tk, 0));
+      if (tk >= 0) {
+        const __half2 f2 = *reinterpret_cast<const __half2*>(&f), ca = __low2half2(f2), cb = __high2half2(f2);
+        const __half2 tlo = __hmul2(cb, lo), thi = __hmul2(cb, hi);
+        const uint32_t code = *reinterpret_cast<const uint16_t*>(cd + x * kCodeBytes);
+        uint4* at = reinterpret_cast<uint4*>(tile + swz(last.q * 32 + tk, c));
         uint4 v = *at;
         uint32_t* vw = reinterpret_cast<uint32_t*>(&v);
-        const __half2 ca = *reinterpret_cast<const __half2*>(&e.y);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           // two codes to the four byte numbers of their table entries
-          const uint32_t n = (code >> (4 * k)) & 15u;
-          const uint32_t sel = ((n | (n << 6)) & 0x303u) * 0x22u + 0x1010u;
-          const uint32_t lv = __byte_perm((uint32_t)e.z, (uint32_t)e.w, sel);
+          const uint32_t nn = (code >> (4 * k)) & 15u;
+          const uint32_t sel = ((nn | (nn << 6)) & 0x303u) * 0x22u + 0x1010u;
+          const uint32_t lv = __byte_perm(*reinterpret_cast<const uint32_t*>(&tlo), *reinterpret_cast<const uint32_t*>(&thi), sel);
           const __half2 y = __hfma2(ca, *reinterpret_cast<const __half2*>(&vw[k]), *reinterpret_cast<const __half2*>(&lv));
           vw[k] = *reinterpret_cast<const uint32_t*>(&y);
         }
         *at = v;
       }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(&p.full[st]);
     }
-    n_rec_last = n_rec;
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.full[last.side][last.tile & 1]);
+    pending = false;
+  };
+
+  for (int id = w; job_of(id).tile < n; id += kProd) {
+    const Job j = job_of(id);
+    const Tok t = t0;
+    const float m = m0, sg = s0;
+    t0 = make_tok(a, r1, tile0, id + kProd);
+    r1 = load_tok(a, comp, h, tile0, n, id + 2 * kProd);
+    m0 = scale_of(t0, id + kProd);
+    s0 = sigma_of(t0);
+    // scale of the row; a residual's row keeps the larger of the two factors at 1
+    const bool res = (t.bits >> lane) & 1u;
+    const float c1 = half_bits_to_f(t.word >> 16) * m;
+    float scale = c1, ca = 1.f, cb = 0.f;
+    if (res) {
+      const bool by_anchor = fabsf(c1) >= sg;
+      scale = by_anchor ? c1 : sg;
+      ca = by_anchor ? 1.f : c1 / sg;
+      cb = by_anchor ? (c1 != 0.f ? sg / c1 : 0.f) : 1.f;
+    }
+    if (j.tile >= 2) {
+      uint64_t* bar = stage_free(sm, j);
+      const uint32_t ph = ((j.tile >> 1) - 1) & 1;
+      // the stage is still being read: finish the job before in the meantime
+      if (pending && !__shfl_sync(0xffffffffu, (int)tc::mbar_done(bar, ph), 0)) {
+        cp_wait<0>();
+        finish(parity ^ 1);
+      }
+      wait_b(sm, bar, ph, a);
+    }
+    job_scales(sm, j, j.q * 32 + lane, scale);   // 0 behind the last token, whose word is 0
+    __syncwarp();
+    if (lane == 0) job_scales_done(sm, j);
+    // rows: sixteen lanes each
+    const uint32_t base = tc::smem_u32(j.side ? sm.V[j.tile & 1] : sm.K[j.tile & 1]);
+    const uint8_t* rows = reinterpret_cast<const uint8_t*>(a.anc) + (row0 + j.side * side_rows) * (kD * 2) + c * 16;
+    const int slot = slot_of(t);
+#pragma unroll
+    for (int r = 0; r < 32; r += 2) {
+      const int s = __shfl_sync(0xffffffffu, slot, r + hw);
+      cp_async16(base + swz(j.q * 32 + r + hw, c), rows + (int64_t)s * (kD * 2));
+    }
+    const uint32_t cd = tc::smem_u32(sm.codes[w][parity]);
+    for (int x = lane; x < 2 * __popc(t.bits); x += 32) cp_async16(cd + x * 16, codes + (int64_t)t.rec * kCodeBytes + x * 16);
+    cp_commit();
+    if (pending) {
+      cp_wait<1>();
+      finish(parity ^ 1);
+    }
+    pending = true;
+    last = j;
+    last_bits = t.bits;
+    last_f = pack_half2(ca, cb);
+    parity ^= 1;
+  }
+  if (pending) {
+    cp_wait<0>();
+    finish(parity ^ 1);
   }
 }
 
 // Exact rows, of pages and drafts: half a warp per row.
-__device__ void produce_tail(const TreeArgs& a, const Prod& p, int b, int h, int tile0, int len, int n_new) {
-  Sm& sm = *p.sm;
-  const int i = p.tid, c = i & 15;
-  const uint16_t* pool = reinterpret_cast<const uint16_t*>(p.side ? a.vp : a.kp);
-  const uint16_t* fresh = reinterpret_cast<const uint16_t*>(p.side ? a.vn : a.kn);
-  for (int j = 0; j < p.n; ++j) {
-    const int st = j % p.stages, u = j / p.stages;
-    if (u > 0) wait_b(sm, &p.empty[st], (u - 1) & 1, a);
-    uint8_t* tile = p.ring + st * kTileBytes;
-    for (int r0 = i >> 4; r0 < kTT; r0 += 32) {
+__device__ void produce_tail(const TreeArgs& a, Sm& sm, int w, int n, int b, int h, int tile0, int len, int n_new) {
+  const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4;
+  for (int id = w; job_of(id).tile < n; id += kProd) {
+    const Job j = job_of(id);
+    const uint16_t* pool = reinterpret_cast<const uint16_t*>(j.side ? a.vp : a.kp);
+    const uint16_t* fresh = reinterpret_cast<const uint16_t*>(j.side ? a.vn : a.kn);
+    if (j.tile >= 2) wait_b(sm, stage_free(sm, j), ((j.tile >> 1) - 1) & 1, a);
+    uint8_t* tile = j.side ? sm.V[j.tile & 1] : sm.K[j.tile & 1];
+    const int first = (tile0 + j.tile) * kTT;
+    for (int r0 = j.q * 32 + hw; r0 < j.q * 32 + 32; r0 += 8) {
       uint4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int t = (tile0 + j) * kTT + r0 + 8 * k;
+        const int t = first + r0 + 2 * k;
         v[k] = make_uint4(0u, 0u, 0u, 0u);
         if (t < len) {
           const int pg = a.table[(int64_t)b * a.maxp + t / a.P];
@@ -363,13 +408,13 @@ __device__ void produce_tail(const TreeArgs& a, const Prod& p, int b, int h, int
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int r = r0 + 8 * k, t = (tile0 + j) * kTT + r;
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[k]);
+        const int r = r0 + 2 * k, t = first + r;
+        const uint32_t* vw = reinterpret_cast<const uint32_t*>(&v[k]);
         float x[8];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          x[2 * y] = __uint_as_float(w[y] << 16);
-          x[2 * y + 1] = __uint_as_float(w[y] & 0xffff0000u);
+          x[2 * y] = __uint_as_float(vw[y] << 16);
+          x[2 * y + 1] = __uint_as_float(vw[y] & 0xffff0000u);
         }
         uint32_t m = 0;
         bool odd = false;
@@ -381,7 +426,7 @@ __device__ void produce_tail(const TreeArgs& a, const Prod& p, int b, int h, int
           odd = odd || !fin;
           // an infinity or NaN in a draft's value must not reach the rows that
           // do not see it (0 x inf): the merge adds it where it is seen
-          if (!fin && p.side && t >= len) x[y] = 0.f;
+          if (!fin && j.side && t >= len) x[y] = 0.f;
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -390,13 +435,16 @@ __device__ void produce_tail(const TreeArgs& a, const Prod& p, int b, int h, int
         *reinterpret_cast<uint4*>(tile + swz(r, c)) =
             make_uint4(pack_half2(x[0] * inv, x[1] * inv), pack_half2(x[2] * inv, x[3] * inv),
                        pack_half2(x[4] * inv, x[5] * inv), pack_half2(x[6] * inv, x[7] * inv));
-        if (odd && p.side && t >= len) atomicOr(&a.inf_v[(int64_t)b * a.H + h], 1ull << (t - len));
-        if (c == 0) (p.side ? sm.wv : sm.rk)[j % p.slots][r] = m ? exp_to_f(e) : (p.side ? 0.f : 1.f);
+        if (odd && j.side && t >= len) atomicOr(&a.inf_v[(int64_t)b * a.H + h], 1ull << (t - len));
+        if (c == 0) job_scales(sm, j, r, m ? exp_to_f(e) : (j.side ? 0.f : 1.f));
       }
     }
     tc::fence_proxy_async_smem();
-    tc::mbar_arrive(&p.scales[j % p.slots]);
-    tc::mbar_arrive(&p.full[st]);
+    __syncwarp();
+    if (lane == 0) {
+      job_scales_done(sm, j);
+      tc::mbar_arrive(&sm.full[j.side][j.tile & 1]);
+    }
   }
 }
 
@@ -406,9 +454,17 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&v)[16]) {
   tc::tmem_wait_ld_dep(v);
 }
 
-// NC: rows (columns of the accumulators) of a CTA.
+// NC: rows (columns of the accumulators) of a CTA, SW: groups of four softmax
+// warps that share them.
 template <int NC>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
+struct Shape {
+  static constexpr int SW = NC == 64 ? 2 : 1, CW = NC / SW;
+  static constexpr int kMma = 4 * SW, kFirstProd = kMma + 1, kThreads = 32 * (kFirstProd + kProd);
+};
+
+template <int NC>
+__global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArgs a) {
+  constexpr int SW = Shape<NC>::SW, CW = Shape<NC>::CW, kMma = Shape<NC>::kMma, kThreads = Shape<NC>::kThreads;
   extern __shared__ __align__(1024) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -439,19 +495,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
   }
 
   // ---- set-up: barriers, tensor memory, queries, masks
-  if (warp == 12) {
+  if (warp == kMma) {
     tc::tmem_alloc(&sm.tmem, kTmemCols);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kKSt; ++i) { tc::mbar_init(&sm.kfull[i], 128); tc::mbar_init(&sm.kempty[i], 1); }
-    for (int i = 0; i < kVSt; ++i) { tc::mbar_init(&sm.vfull[i], 128); tc::mbar_init(&sm.sv[i], 128); }
-    for (int i = 0; i < kKSl; ++i) tc::mbar_init(&sm.sk[i], 128);
+    for (int i = 0; i < kKSl; ++i) tc::mbar_init(&sm.sk[i], 4);          // four quarters of a tile
+    for (int i = 0; i < kVSt; ++i) tc::mbar_init(&sm.sv[i], 4);
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.full[0][i], 4);
+      tc::mbar_init(&sm.full[1][i], 4);
+      tc::mbar_init(&sm.kempty[i], 1);
       tc::mbar_init(&sm.pv[i], 1);
       tc::mbar_init(&sm.sfull[i], 1);
-      tc::mbar_init(&sm.sempty[i], 128);
-      tc::mbar_init(&sm.pfull[i], 128);
+      tc::mbar_init(&sm.sempty[i], 4 * SW);                              // one arrival a warp
+      tc::mbar_init(&sm.pfull[i], 4 * SW);
     }
     tc::fence_barrier_init();
     sm.err = 0;
@@ -500,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = sm.tmem;
 
-  if (warp == 12) {
+  if (warp == kMma) {
     // ---- MMA issue
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16(128, NC, 0, 0), id_o = idesc_f16(128, kOCols, 1, 1);
@@ -508,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
       for (int i = 0; i <= n; ++i) {
         if (i < n) {
           const int st = i % kKSt, bf = i & 1;
-          wait_b(sm, &sm.kfull[st], (i / kKSt) & 1, a);
+          wait_b(sm, &sm.full[0][st], (i / kKSt) & 1, a);
           if (i >= 2) wait_b(sm, &sm.sempty[bf], ((i >> 1) - 1) & 1, a);
           tc::fence_after_sync();
           if (!*(volatile int*)&sm.err) {
@@ -523,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
         }
         if (i > 0) {
           const int o = i - 1, st = o % kVSt;
-          wait_b(sm, &sm.vfull[st], (o / kVSt) & 1, a);
+          wait_b(sm, &sm.full[1][st], (o / kVSt) & 1, a);
           wait_b(sm, &sm.pfull[o & 1], (o >> 1) & 1, a);
           tc::fence_after_sync();
           if (!*(volatile int*)&sm.err) {
@@ -537,34 +595,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp > kMma) {
     // ---- rows of the key and value tiles
-    Prod p;
-    p.sm = &sm;
-    p.side = warp >= 8;
-    p.tid = tid & 127;
-    p.n = n;
-    p.ring = p.side ? sm.V[0] : sm.K[0];
-    p.full = p.side ? sm.vfull : sm.kfull;
-    p.empty = p.side ? sm.pv : sm.kempty;
-    p.scales = p.side ? sm.sv : sm.sk;
-    p.stages = 2;
-    p.slots = p.side ? kVSt : kKSl;
-    if (tail) produce_tail(a, p, b, h, tile0, len, n_new);
-    else produce_prefix(a, p, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0);
+    const int w = warp - Shape<NC>::kFirstProd;
+    if (tail) produce_tail(a, sm, w, n, b, h, tile0, len, n_new);
+    else produce_prefix(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0);
   } else {
-    // ---- softmax: thread = token
-    constexpr int CW = NC < 32 ? NC : 32, CH = NC / CW;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    float2 lacc[CH][CW / 2];
+    // ---- softmax: thread = token, a group of four warps has CW of the rows
+    const int tok = tid & 127, wq = warp & 3, c0 = (warp >> 2) * CW, bar_id = 1 + (warp >> 2);
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    float2 lacc[CW / 2];
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int x = 0; x < CW / 2; ++x) lacc[c][x] = make_float2(0.f, 0.f);
+    for (int x = 0; x < CW / 2; ++x) lacc[x] = make_float2(0.f, 0.f);
     for (int i = 0; i < n; ++i) {
       const int bf = i & 1;
       // what this token is, and who sees it
-      const int t = (tile0 + i) * kTT + tid;
+      const int t = (tile0 + i) * kTT + tok;
       bool special = false, live = true;
       unsigned long long vis = ~0ull;
       if (tail) {
@@ -581,151 +627,149 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
       if (!live) vis = 0;
       wait_b(sm, &sm.sk[i % kKSl], (i / kKSl) & 1, a);
       wait_b(sm, &sm.sv[i % kVSt], (i / kVSt) & 1, a);
-      const float rk = sm.rk[i % kKSl][tid], w = sm.wv[i % kVSt][tid];
+      const float rk = sm.rk[i % kKSl][tok], w = sm.wv[i % kVSt][tok];
       wait_b(sm, &sm.sfull[bf], (i >> 1) & 1, a);
       tc::fence_after_sync();
-      if (i >= 2) wait_b(sm, &sm.pv[bf], ((i >> 1) - 1) & 1, a);
-      const uint32_t scol = tmem + lane_base + kOCols + bf * NC;
-      uint8_t* prow = sm.P[bf] + tid * 128;
+      const uint32_t scol = tmem + lane_base + kOCols + bf * NC + c0;
+      uint8_t* prow = sm.P[bf] + tok * 128;
+      float2 p[CW / 2];
+      uint32_t pk[CW / 2];
+      auto exponentials = [&]() {
+        float pmax = 0.f, vmax = 0.f;
 #pragma unroll
-      for (int ch = 0; ch < CH; ++ch) {
-        const int c0 = ch * CW;
-        float2 p[CW / 2];
-        uint32_t pk[CW / 2];
-        auto exponentials = [&]() {
-          float pmax = 0.f, vmax = 0.f;
+        for (int x = 0; x < CW; x += 16) {
+          uint32_t s[16];
+          load_cols(scol + x, s);
 #pragma unroll
-          for (int x = 0; x < CW; x += 16) {
-            uint32_t s[16];
-            load_cols(scol + c0 + x, s);
+          for (int y = 0; y < 16; y += 4) {
+            const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c0 + x + y]);
+            const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[c0 + x + y]);
+            const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[c0 + x + y]);
 #pragma unroll
-            for (int y = 0; y < 16; y += 4) {
-              const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c0 + x + y]);
-              const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[c0 + x + y]);
-              const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[c0 + x + y]);
-#pragma unroll
-              for (int z = 0; z < 4; z += 2) {
-                const float2 k2 = __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk));
-                float2 u = __ffma2_rn(make_float2(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 1])), k2,
-                                      z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
-                if (special) {
-                  if (!((vis >> sm.colt[c0 + x + y + z]) & 1ull)) u.x = -INFINITY;
-                  if (!((vis >> sm.colt[c0 + x + y + z + 1]) & 1ull)) u.y = -INFINITY;
-                }
-                const float2 e = make_float2(tc::ex2_approx(u.x), tc::ex2_approx(u.y));
-                // in this order a masked 0 stays 0 whatever the value's scale
-                const float2 v = __fmul2_rn(__fmul2_rn(e, make_float2(w, w)),
-                                            z ? make_float2(cw.z, cw.w) : make_float2(cw.x, cw.y));
-                pmax = fmaxf(pmax, fmaxf(e.x, e.y));
-                vmax = fmaxf(vmax, fmaxf(fabsf(v.x), fabsf(v.y)));
-                p[(x + y + z) / 2] = e;
-                pk[(x + y + z) / 2] = pack_half2(v.x, v.y);
+            for (int z = 0; z < 4; z += 2) {
+              const float2 k2 = __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk));
+              float2 u = __ffma2_rn(make_float2(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 1])), k2,
+                                    z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
+              if (special) {
+                if (!((vis >> sm.colt[c0 + x + y + z]) & 1ull)) u.x = -INFINITY;
+                if (!((vis >> sm.colt[c0 + x + y + z + 1]) & 1ull)) u.y = -INFINITY;
               }
+              const float2 e = make_float2(tc::ex2_approx(u.x), tc::ex2_approx(u.y));
+              // in this order a masked 0 stays 0 whatever the value's scale
+              const float2 v = __fmul2_rn(__fmul2_rn(e, make_float2(w, w)),
+                                          z ? make_float2(cw.z, cw.w) : make_float2(cw.x, cw.y));
+              pmax = fmaxf(pmax, fmaxf(e.x, e.y));
+              vmax = fmaxf(vmax, fmaxf(fabsf(v.x), fabsf(v.y)));
+              p[(x + y + z) / 2] = e;
+              pk[(x + y + z) / 2] = pack_half2(v.x, v.y);
             }
           }
-          return pmax > kSumLimit || vmax > kPLimit;
-        };
-        if (bar_or(1, 128, exponentials())) {
-          // ---- new references for these rows (the first tile, and rarely after)
-          const float lw = w != 0.f ? __log2f(fabsf(w)) : -INFINITY;
-#pragma unroll 1
-          for (int x = 0; x < CW; x += 16) {
-            uint32_t s[16];
-            load_cols(scol + c0 + x, s);
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const int c = c0 + x + y;
-              const bool seen = !special || ((vis >> sm.colt[c]) & 1ull);
-              const float lg = seen ? __uint_as_float(s[y]) * (rk * sm.cs[c]) : -INFINITY;
-              const int m1 = __reduce_max_sync(0xffffffffu, ordered(lg));
-              const int m2 = __reduce_max_sync(0xffffffffu, ordered(lg + lw));
-              if (lane == 0) {
-                sm.red[0][warp][x + y] = m1;
-                sm.red[1][warp][x + y] = m2;
-              }
-            }
-          }
-          tc::named_bar(1, 128);
-          if (tid < CW) {
-            const int c = c0 + tid;
-            const float m1 = unordered(max(max(sm.red[0][0][tid], sm.red[0][1][tid]), max(sm.red[0][2][tid], sm.red[0][3][tid])));
-            const float m2 = unordered(max(max(sm.red[1][0][tid], sm.red[1][1][tid]), max(sm.red[1][2][tid], sm.red[1][3][tid])));
-            const float l_old = -sm.nm[c], p_old = sm.mp[c];
-            const float l_new = fmaxf(l_old, ceilf(m1));
-            float p_new = fmaxf(p_old, ceilf(m2));
-            if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
-            sm.fl[c] = l_old > -INFINITY ? exp2f(l_old - l_new) : 0.f;
-            sm.fp[c] = p_old > -INFINITY ? exp2f(p_old - p_new) : 0.f;
-            sm.nm[c] = -l_new;
-            sm.mp[c] = p_new;
-            sm.cw[c] = l_new > -INFINITY ? exp2f(l_new - p_new) : 1.f;
-          }
-          tc::named_bar(1, 128);
-#pragma unroll
-          for (int x = 0; x < CW / 2; ++x) {
-            lacc[ch][x].x *= sm.fl[c0 + 2 * x];
-            lacc[ch][x].y *= sm.fl[c0 + 2 * x + 1];
-          }
-          if (i > 0) {
-            wait_b(sm, &sm.pv[(i - 1) & 1], ((i - 1) >> 1) & 1, a);
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int x = 0; x < CW; x += 16) {
-              uint32_t o[16];
-              load_cols(tmem + lane_base + c0 + x, o);
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * sm.fp[c0 + x + y]);
-              tmem_st16(tmem + lane_base + c0 + x, o);
-            }
-            tmem_wait_st();
-          }
-          exponentials();
         }
+        return pmax > kSumLimit || vmax > kPLimit;
+      };
+      if (bar_or(bar_id, 128, exponentials())) {
+        // ---- new references for these rows (the first tile, and rarely after)
+        const float lw = w != 0.f ? __log2f(fabsf(w)) : -INFINITY;
+#pragma unroll 1
+        for (int x = 0; x < CW; x += 16) {
+          uint32_t s[16];
+          load_cols(scol + x, s);
 #pragma unroll
-        for (int x = 0; x < CW / 2; ++x) lacc[ch][x] = __fadd2_rn(lacc[ch][x], p[x]);
+          for (int y = 0; y < 16; ++y) {
+            const int c = c0 + x + y;
+            const bool seen = !special || ((vis >> sm.colt[c]) & 1ull);
+            const float lg = seen ? __uint_as_float(s[y]) * (rk * sm.cs[c]) : -INFINITY;
+            const int m1 = __reduce_max_sync(0xffffffffu, ordered(lg));
+            const int m2 = __reduce_max_sync(0xffffffffu, ordered(lg + lw));
+            if (lane == 0) {
+              sm.red[0][wq][c] = m1;
+              sm.red[1][wq][c] = m2;
+            }
+          }
+        }
+        tc::named_bar(bar_id, 128);
+        if (tok < CW) {
+          const int c = c0 + tok;
+          const float m1 = unordered(max(max(sm.red[0][0][c], sm.red[0][1][c]), max(sm.red[0][2][c], sm.red[0][3][c])));
+          const float m2 = unordered(max(max(sm.red[1][0][c], sm.red[1][1][c]), max(sm.red[1][2][c], sm.red[1][3][c])));
+          const float l_old = -sm.nm[c], p_old = sm.mp[c];
+          const float l_new = fmaxf(l_old, ceilf(m1));
+          float p_new = fmaxf(p_old, ceilf(m2));
+          if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
+          sm.fl[c] = l_old > -INFINITY ? exp2f(l_old - l_new) : 0.f;
+          sm.fp[c] = p_old > -INFINITY ? exp2f(p_old - p_new) : 0.f;
+          sm.nm[c] = -l_new;
+          sm.mp[c] = p_new;
+          sm.cw[c] = l_new > -INFINITY ? exp2f(l_new - p_new) : 1.f;
+        }
+        tc::named_bar(bar_id, 128);
 #pragma unroll
-        for (int x = 0; x < CW / 8; ++x)
-          *reinterpret_cast<uint4*>(prow + (((c0 / 8 + x) ^ (tid & 7)) << 4)) =
-              make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+        for (int x = 0; x < CW / 2; ++x) {
+          lacc[x].x *= sm.fl[c0 + 2 * x];
+          lacc[x].y *= sm.fl[c0 + 2 * x + 1];
+        }
+        if (i > 0) {
+          wait_b(sm, &sm.pv[(i - 1) & 1], ((i - 1) >> 1) & 1, a);
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int x = 0; x < CW; x += 16) {
+            uint32_t o[16];
+            load_cols(tmem + lane_base + c0 + x, o);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * sm.fp[c0 + x + y]);
+            tmem_st16(tmem + lane_base + c0 + x, o);
+          }
+          tmem_wait_st();
+        }
+        exponentials();
       }
+#pragma unroll
+      for (int x = 0; x < CW / 2; ++x) lacc[x] = __fadd2_rn(lacc[x], p[x]);
+      if (i >= 2) wait_b(sm, &sm.pv[bf], ((i >> 1) - 1) & 1, a);   // the outputs that read this buffer of P
+#pragma unroll
+      for (int x = 0; x < CW / 8; ++x)
+        *reinterpret_cast<uint4*>(prow + (((c0 / 8 + x) ^ (tok & 7)) << 4)) =
+            make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      tc::mbar_arrive(&sm.sempty[bf]);
-      tc::mbar_arrive(&sm.pfull[bf]);
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&sm.sempty[bf]);
+        tc::mbar_arrive(&sm.pfull[bf]);
+      }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- sums over the tokens, outputs in units of the sums' references
-#pragma unroll
-    for (int ch = 0; ch < CH; ++ch) {
+    {
       float v[32];
 #pragma unroll
-      for (int x = 0; x < 32; ++x) v[x] = x < CW ? (x & 1 ? lacc[ch][(x < CW ? x : 0) / 2].y : lacc[ch][(x < CW ? x : 0) / 2].x) : 0.f;
+      for (int x = 0; x < 32; ++x) v[x] = x < CW ? (x & 1 ? lacc[(x < CW ? x : 0) / 2].y : lacc[(x < CW ? x : 0) / 2].x) : 0.f;
       transpose_reduce32(v, lane);
-      if (lane < CW) sm.lsum[warp][ch * CW + lane] = v[0];
+      if (lane < CW) sm.lsum[wq][c0 + lane] = v[0];
     }
-    tc::named_bar(1, 128);
+    tc::named_bar(bar_id, 128);
     wait_b(sm, &sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, a);
     tc::fence_after_sync();
     const bool nan = *(volatile int*)&sm.err || *(volatile int*)&sm.bad;
     if (nan && tid == 0) latch_error(a.counters, kDevErrBounds);
-    if (tid < NC) {
-      ml[2 * tid] = nan ? 0.f : -sm.nm[tid];
-      ml[2 * tid + 1] =
-          nan ? __int_as_float(0x7fc00000) : sm.lsum[0][tid] + sm.lsum[1][tid] + sm.lsum[2][tid] + sm.lsum[3][tid];
+    if (tok < CW) {
+      const int c = c0 + tok;
+      ml[2 * c] = nan ? 0.f : -sm.nm[c];
+      ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : sm.lsum[0][c] + sm.lsum[1][c] + sm.lsum[2][c] + sm.lsum[3][c];
     }
-    float* o = a.part + (unit * a.parts + part) * NC * kD + tid;
+    float* o = a.part + ((unit * a.parts + part) * NC + c0) * kD + tok;
 #pragma unroll 1
-    for (int x = 0; x < NC; x += 16) {
+    for (int x = 0; x < CW; x += 16) {
       uint32_t v[16];
-      load_cols(tmem + lane_base + x, v);
+      load_cols(tmem + lane_base + c0 + x, v);
 #pragma unroll
-      for (int y = 0; y < 16; ++y) o[(x + y) * kD] = __uint_as_float(v[y]) * exp2f(sm.mp[x + y] + sm.nm[x + y]);
+      for (int y = 0; y < 16; ++y) o[(x + y) * kD] = __uint_as_float(v[y]) * exp2f(sm.mp[c0 + x + y] + sm.nm[c0 + x + y]);
     }
     tc::fence_before_sync();
   }
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 12) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMma) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 // One warp per output row: the parts joined by their references and sums, the
@@ -824,7 +868,7 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   const int gx = a.comp ? std::max(1, std::min((a.k + 7) / 8, 256)) : 1;
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  int st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), kThreads, kSmem, a, s);
+  int st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, a, s);
   if (st) return st;
   const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
   return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 7) / 8)), 256, 0, a, s);
