@@ -41,6 +41,10 @@
 // rescaling exact, so the result does not depend on when it happens.
 //
 // Bound by the anchor rows' way from L2 (64 KB a tile).
+#include <cudaTypedefs.h>
+
+#include <stddef.h>
+
 #include <algorithm>
 #include <mutex>
 
@@ -72,10 +76,11 @@ struct Sm {
   uint8_t V[kVSt][kTileBytes];
   uint8_t P[2][kTT * 128];                // [token][64 rows] fp16, swizzled
   uint8_t Q[64 * kD * 2];
-  uint8_t codes[kProd][2][32 * kCodeBytes];   // of a producer's job and the one before
+  alignas(16) uint8_t codes[kProd][2][32 * kCodeBytes];   // of a producer's job and the one before
+  uint64_t landed[kProd][2], drain;       // their copies; products after a failure
   float rk[kKSl][kTT];                    // key scales
   float wv[kVSt][kTT];                    // value scales
-  float cs[64], nm[64], cw[64], mp[64];   // per row: logit scale, -reference of the sum, 2^(sum's - w p's), w p's
+  alignas(16) float cs[64], nm[64], cw[64], mp[64];   // (read four at a time) per row: logit scale, -reference of the sum, 2^(sum's - w p's), w p's
   float fl[64], fp[64];                   // rescaling factors
   int red[2][4][64];
   float lsum[4][64];
@@ -85,13 +90,27 @@ struct Sm {
   uint32_t tmem;
   int err, bad, rep;
 };
+static_assert(offsetof(Sm, cs) % 16 == 0 && offsetof(Sm, nm) % 16 == 0 && offsetof(Sm, cw) % 16 == 0 &&
+              offsetof(Sm, codes) % 16 == 0 && offsetof(Sm, V) % 1024 == 0 && offsetof(Sm, P) % 1024 == 0 &&
+              offsetof(Sm, Q) % 1024 == 0, "16-byte reads, swizzle atoms");
 static_assert(kVSt == 2, "the value ring and the P buffers share the barrier pv");
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Four rows (y) of 64 columns from x on, 128 bytes each, swizzled like a tile.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, int y0, int y1, int y2, int y3,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// `bytes` (a multiple of 16) from a 16-byte aligned address.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -115,6 +134,13 @@ __device__ __forceinline__ uint32_t bar_or(int id, int count, bool p) {
       : "r"(id), "r"(count), "r"((uint32_t)p)
       : "memory");
   return r;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -202,13 +228,18 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {   // byte offset o
   return (uint32_t)((chunk >> 3) * kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-// Work of a producer warp: 32 rows of one tile and side.  Jobs are numbered
-// tile by tile (four quarters of the keys, four of the values) and go round
-// the producer warps, which need nothing from one another.
+// Work of a producer warp: 32 rows of one tile and side.  Jobs go round the
+// producer warps, which need nothing from one another, four quarters at a
+// time: keys of tile 0, keys 1, values 0, keys 2, values 1, ...  The keys are a
+// tile ahead so that a value job waiting for its stage holds up no logits.
 struct Job {
   int tile, side, q;                      // tile of this CTA's share, quarter
 };
-__device__ __forceinline__ Job job_of(int id) { return Job{id >> 3, (id >> 2) & 1, id & 3}; }
+__device__ __forceinline__ Job job_of(int id) {
+  const int s = id >> 2, v = s > 0 && !(s & 1);
+  return Job{v ? (s >> 1) - 1 : (s + 1) >> 1, v, id & 3};
+}
+__device__ __forceinline__ int job_count(int n) { return 8 * n + 4; }   // among them four of a key tile that is not there
 
 // The job's stage is free: the products that read its last tile are done
 // (keys: the logits, values: the outputs).
@@ -260,8 +291,11 @@ __device__ __forceinline__ Tok make_tok(const TreeArgs& a, const Raw& r, int til
   return t;
 }
 
-__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* comp, int rep, int h, int tile0) {
-  const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4;
+__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* comp, int rep, int h, int tile0,
+                               const CUtensorMap* map) {
+  const int lane = threadIdx.x & 31, c = lane & 7, g = lane >> 3;
+  const __half l0 = __float2half_rn(a.lev[0]), l1 = __float2half_rn(a.lev[1]);
+  const __half2 lo = __halves2half2(l0, l1), hi = __halves2half2(__hneg(l1), __hneg(l0));
   const int64_t row0 = ((int64_t)rep * 2 * a.H + h) * a.k, side_rows = (int64_t)a.H * a.k;
   const uint8_t* codes = comp + a.off_codes;
   const uint16_t* sig = reinterpret_cast<const uint16_t*>(comp + a.off_sig);
@@ -280,39 +314,55 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
   bool pending = false;
   Job last = {};
   uint32_t last_bits = 0, last_f = 0;
-  int parity = 0;
+  int issued = 0;                         // jobs of this warp: buffer and phase of their copies
 
-  auto finish = [&](uint32_t buf) {
+  // completes the last job issued
+  auto finish = [&](int k) {
+    const int buf = k & 1;
     uint8_t* tile = last.side ? sm.V[last.tile & 1] : sm.K[last.tile & 1];
     const uint8_t* cd = sm.codes[w][buf] + c * 2;
-    const __half l0 = __float2half_rn(a.lev[0]), l1 = __float2half_rn(a.lev[1]);
-    const __half2 lo = __halves2half2(l0, l1), hi = __halves2half2(__hneg(l1), __hneg(l0));
-    __syncwarp();                                          // the whole warp's copies have landed
-    int x = hw;
-    for (uint32_t m = last_bits; m; x += 2) {
-      const int b0 = __ffs(m) - 1;
-      m &= m - 1;
-      const int b1 = m ? __ffs(m) - 1 : -1;
-      m &= m - 1;
-      const int tk = hw ? b1 : b0;
+    // bounded, and not cut short where another role has failed: the copies
+    // have to be over before this CTA's shared memory is
+    if (!tc::mbar_done(&sm.landed[w][buf], (k >> 1) & 1) && !tc::mbar_wait(&sm.landed[w][buf], (k >> 1) & 1)) {
+      *(volatile int*)&sm.err = 1;
+      latch_error(a.counters, kDevErrTimeout);
+    }
+    // four records at a time, eight lanes each, two 16-byte pieces a lane
+    int x = g;
+    for (uint32_t m = last_bits; m; x += 4) {
+      int tk = -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k == g && m) tk = __ffs(m) - 1;
+        m &= m - 1;
+      }
       const uint32_t f = __shfl_sync(0xffffffffu, last_f, max(tk, 0));
       if (tk >= 0) {
         const __half2 f2 = *reinterpret_cast<const __half2*>(&f), ca = __low2half2(f2), cb = __high2half2(f2);
         const __half2 tlo = __hmul2(cb, lo), thi = __hmul2(cb, hi);
-        const uint32_t code = *reinterpret_cast<const uint16_t*>(cd + x * kCodeBytes);
-        uint4* at = reinterpret_cast<uint4*>(tile + swz(last.q * 32 + tk, c));
-        uint4 v = *at;
-        uint32_t* vw = reinterpret_cast<uint32_t*>(&v);
+        const uint32_t t01 = *reinterpret_cast<const uint32_t*>(&tlo), t23 = *reinterpret_cast<const uint32_t*>(&thi);
+        uint8_t* row = tile + swz(last.q * 32 + tk, c);
+        uint32_t code[2];
+        uint4 v[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // two codes to the four byte numbers of their table entries
-          const uint32_t nn = (code >> (4 * k)) & 15u;
-          const uint32_t sel = ((nn | (nn << 6)) & 0x303u) * 0x22u + 0x1010u;
-          const uint32_t lv = __byte_perm(*reinterpret_cast<const uint32_t*>(&tlo), *reinterpret_cast<const uint32_t*>(&thi), sel);
-          const __half2 y = __hfma2(ca, *reinterpret_cast<const __half2*>(&vw[k]), *reinterpret_cast<const __half2*>(&lv));
-          vw[k] = *reinterpret_cast<const uint32_t*>(&y);
+        for (int y = 0; y < 2; ++y) {
+          code[y] = *reinterpret_cast<const uint16_t*>(cd + x * kCodeBytes + y * 16);
+          v[y] = *reinterpret_cast<const uint4*>(row + y * kHalf);
         }
-        *at = v;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t* vw = reinterpret_cast<uint32_t*>(&v[y]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // two codes to the four byte numbers of their table entries
+            const uint32_t nn = (code[y] >> (4 * k)) & 15u;
+            const uint32_t sel = ((nn | (nn << 6)) & 0x303u) * 0x22u + 0x1010u;
+            const uint32_t lv = __byte_perm(t01, t23, sel);
+            const __half2 z = __hfma2(ca, *reinterpret_cast<const __half2*>(&vw[k]), *reinterpret_cast<const __half2*>(&lv));
+            vw[k] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          *reinterpret_cast<uint4*>(row + y * kHalf) = v[y];
+        }
       }
     }
     tc::fence_proxy_async_smem();
@@ -321,7 +371,7 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
     pending = false;
   };
 
-  for (int id = w; job_of(id).tile < n; id += kProd) {
+  for (int id = w; id < job_count(n); id += kProd) {
     const Job j = job_of(id);
     const Tok t = t0;
     const float m = m0, sg = s0;
@@ -336,55 +386,51 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
     if (res) {
       const bool by_anchor = fabsf(c1) >= sg;
       scale = by_anchor ? c1 : sg;
-      ca = by_anchor ? 1.f : c1 / sg;
-      cb = by_anchor ? (c1 != 0.f ? sg / c1 : 0.f) : 1.f;
+      ca = by_anchor ? 1.f : __fdividef(c1, sg);
+      cb = by_anchor ? (c1 != 0.f ? __fdividef(sg, c1) : 0.f) : 1.f;
     }
+    if (j.tile >= n) continue;
     if (j.tile >= 2) {
       uint64_t* bar = stage_free(sm, j);
       const uint32_t ph = ((j.tile >> 1) - 1) & 1;
       // the stage is still being read: finish the job before in the meantime
-      if (pending && !__shfl_sync(0xffffffffu, (int)tc::mbar_done(bar, ph), 0)) {
-        cp_wait<0>();
-        finish(parity ^ 1);
-      }
+      if (pending && !__shfl_sync(0xffffffffu, (int)tc::mbar_done(bar, ph), 0)) finish(issued - 1);
       wait_b(sm, bar, ph, a);
     }
     job_scales(sm, j, j.q * 32 + lane, scale);   // 0 behind the last token, whose word is 0
     __syncwarp();
     if (lane == 0) job_scales_done(sm, j);
-    // rows: sixteen lanes each
+    // anchor rows by slot, four rows and half their coordinates a copy; the
+    // residuals' codes as one block
     const uint32_t base = tc::smem_u32(j.side ? sm.V[j.tile & 1] : sm.K[j.tile & 1]);
-    const uint8_t* rows = reinterpret_cast<const uint8_t*>(a.anc) + (row0 + j.side * side_rows) * (kD * 2) + c * 16;
-    const int slot = slot_of(t);
+    const int row = (int)(row0 + j.side * side_rows) + slot_of(t);
+    int y[4];
 #pragma unroll
-    for (int r = 0; r < 32; r += 2) {
-      const int s = __shfl_sync(0xffffffffu, slot, r + hw);
-      cp_async16(base + swz(j.q * 32 + r + hw, c), rows + (int64_t)s * (kD * 2));
-    }
-    const uint32_t cd = tc::smem_u32(sm.codes[w][parity]);
-    for (int x = lane; x < 2 * __popc(t.bits); x += 32) cp_async16(cd + x * 16, codes + (int64_t)t.rec * kCodeBytes + x * 16);
-    cp_commit();
-    if (pending) {
-      cp_wait<1>();
-      finish(parity ^ 1);
-    }
+    for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, c * 4 + k);
+    const int parity = issued & 1;
+    const uint32_t bar = tc::smem_u32(&sm.landed[w][parity]), n_codes = kCodeBytes * __popc(t.bits);
+    if (lane == 0) tc::mbar_expect_tx(&sm.landed[w][parity], 32 * kD * 2 + n_codes);
+    __syncwarp();
+    if (lane < 16)
+      gather4(base + g * kHalf + (j.q * 32 + c * 4) * 128, map, g * 64, y[0], y[1], y[2], y[3], bar);
+    if (lane == 16 && n_codes)
+      bulk_copy(tc::smem_u32(sm.codes[w][parity]), codes + (int64_t)t.rec * kCodeBytes, n_codes, bar);
+    if (pending) finish(issued - 1);
+    ++issued;
     pending = true;
     last = j;
     last_bits = t.bits;
     last_f = pack_half2(ca, cb);
-    parity ^= 1;
   }
-  if (pending) {
-    cp_wait<0>();
-    finish(parity ^ 1);
-  }
+  if (pending) finish(issued - 1);
 }
 
 // Exact rows, of pages and drafts: half a warp per row.
 __device__ void produce_tail(const TreeArgs& a, Sm& sm, int w, int n, int b, int h, int tile0, int len, int n_new) {
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4;
-  for (int id = w; job_of(id).tile < n; id += kProd) {
+  for (int id = w; id < job_count(n); id += kProd) {
     const Job j = job_of(id);
+    if (j.tile >= n) continue;
     const uint16_t* pool = reinterpret_cast<const uint16_t*>(j.side ? a.vp : a.kp);
     const uint16_t* fresh = reinterpret_cast<const uint16_t*>(j.side ? a.vn : a.kn);
     if (j.tile >= 2) wait_b(sm, stage_free(sm, j), ((j.tile >> 1) - 1) & 1, a);
@@ -463,7 +509,7 @@ struct Shape {
 };
 
 template <int NC>
-__global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int SW = Shape<NC>::SW, CW = Shape<NC>::CW, kMma = Shape<NC>::kMma, kThreads = Shape<NC>::kThreads;
   extern __shared__ __align__(1024) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -502,6 +548,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   if (tid == 0) {
     for (int i = 0; i < kKSl; ++i) tc::mbar_init(&sm.sk[i], 4);          // four quarters of a tile
     for (int i = 0; i < kVSt; ++i) tc::mbar_init(&sm.sv[i], 4);
+    for (int i = 0; i < 2 * kProd; ++i) tc::mbar_init(&sm.landed[0][0] + i, 1);
+    tc::mbar_init(&sm.drain, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.full[0][i], 4);
       tc::mbar_init(&sm.full[1][i], 4);
@@ -560,7 +608,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
 
   if (warp == kMma) {
     // ---- MMA issue
-    if (lane == 0) {
+    {
+      const bool one = elect_one();
       constexpr uint32_t id_s = idesc_f16(128, NC, 0, 0), id_o = idesc_f16(128, kOCols, 1, 1);
       const uint32_t kb = tc::smem_u32(sm.K), vb = tc::smem_u32(sm.V), pb = tc::smem_u32(sm.P), qb = tc::smem_u32(sm.Q);
       for (int i = 0; i <= n; ++i) {
@@ -569,7 +618,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
           wait_b(sm, &sm.full[0][st], (i / kKSt) & 1, a);
           if (i >= 2) wait_b(sm, &sm.sempty[bf], ((i >> 1) - 1) & 1, a);
           tc::fence_after_sync();
-          if (!*(volatile int*)&sm.err) {
+          if (one && !*(volatile int*)&sm.err) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
               tc::mma_bf16(tmem + kOCols + bf * NC,
@@ -584,7 +633,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
           wait_b(sm, &sm.full[1][st], (o / kVSt) & 1, a);
           wait_b(sm, &sm.pfull[o & 1], (o >> 1) & 1, a);
           tc::fence_after_sync();
-          if (!*(volatile int*)&sm.err) {
+          if (one && !*(volatile int*)&sm.err) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
               tc::mma_bf16(tmem, tc::sw128_mn_desc(vb + st * kTileBytes + ks * 2048, kHalf),
@@ -593,13 +642,18 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
           }
         }
       }
+      // after a failure nobody waits for the products in flight: do it here
+      if (*(volatile int*)&sm.err) {
+        if (one) tc::mma_commit(&sm.drain);
+        tc::mbar_wait(&sm.drain, 0);
+      }
     }
     __syncwarp();
   } else if (warp > kMma) {
     // ---- rows of the key and value tiles
     const int w = warp - Shape<NC>::kFirstProd;
     if (tail) produce_tail(a, sm, w, n, b, h, tile0, len, n_new);
-    else produce_prefix(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0);
+    else produce_prefix(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0, &map);
   } else {
     // ---- softmax: thread = token, a group of four warps has CW of the rows
     const int tok = tid & 127, wq = warp & 3, c0 = (warp >> 2) * CW, bar_id = 1 + (warp >> 2);
@@ -833,8 +887,8 @@ __global__ void __launch_bounds__(256) tree_tc_merge_kernel(TreeArgs a) {
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <typename K>
-int launch_dependent(K kernel, dim3 grid, int threads, int smem, const TreeArgs& a, cudaStream_t s) {
+template <typename K, typename... Args>
+int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -845,7 +899,25 @@ int launch_dependent(K kernel, dim3 grid, int threads, int smem, const TreeArgs&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? ANCHORKV_OK : ANCHORKV_ECUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ANCHORKV_OK : ANCHORKV_ECUDA;
+}
+
+// The rotated anchors as rows of D fp16, gathered four rows and 64 columns at
+// a time (a gather's box is one row high).
+bool anchor_map(CUtensorMap* m, const void* base, int64_t rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {kD, (cuuint64_t)rows}, strides[1] = {kD * 2};
+  const cuuint32_t box[2] = {64, 1}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int kSmem = (int)sizeof(Sm) + 1024;
@@ -865,13 +937,15 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
       ready_dev = dev;
     }
   }
+  CUtensorMap map;
+  if (!anchor_map(&map, a.anc, (int64_t)a.batch * 2 * a.H * a.k)) return ANCHORKV_ECUDA;
   const int gx = a.comp ? std::max(1, std::min((a.k + 7) / 8, 256)) : 1;
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  int st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, a, s);
+  int st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, s, a, map);
   if (st) return st;
   const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
-  return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 7) / 8)), 256, 0, a, s);
+  return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 7) / 8)), 256, 0, s, a);
 }
 
 }  // namespace
