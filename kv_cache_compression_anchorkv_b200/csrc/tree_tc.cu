@@ -31,9 +31,9 @@
 //   softmax, 4 warps for 16 or 32 rows and 8 for 64: logits from tensor
 //     memory, exponentials, P to shared memory; at the end the outputs
 //   one warp issues the MMAs
-//   7 warps fill key and value tiles, 32 rows a job: anchor rows by 16-byte
-//     asynchronous copies into the 128-byte swizzle, residual rows finished in
-//     place (half a warp each), one job behind the copies
+//   16 or 8 warps fill key and value tiles, 32 rows each: anchor rows by
+//     16-byte asynchronous copies into the 128-byte swizzle, residual rows
+//     finished in place (eight lanes each)
 // The maximum over tokens would need a reduction across lanes for every row
 // and tile.  Instead each row keeps two power-of-two references, one for the
 // sum of p and one for w p (the fp16 operand), which move only when a tile
@@ -41,7 +41,6 @@
 // rescaling exact, so the result does not depend on when it happens.
 //
 // Bound by the anchor rows' way from L2 (64 KB a tile).
-#include <cudaTypedefs.h>
 
 #include <stddef.h>
 
@@ -56,7 +55,7 @@ namespace akv {
 namespace {
 
 constexpr int kTT = 128;                  // tokens of a tile
-constexpr int kProd = 7;                  // producer warps
+constexpr int kMaxProd = 16;              // producer warps
 constexpr int kKSt = 2, kVSt = 2;         // stages of the key and value rings
 constexpr int kKSl = kKSt + 2;            // key scales outlive their tile by the two logit buffers
 constexpr int kTileBytes = kTT * kD * 2;
@@ -76,8 +75,8 @@ struct Sm {
   uint8_t V[kVSt][kTileBytes];
   uint8_t P[2][kTT * 128];                // [token][64 rows] fp16, swizzled
   uint8_t Q[64 * kD * 2];
-  alignas(16) uint8_t codes[kProd][2][32 * kCodeBytes];   // of a producer's job and the one before
-  uint64_t landed[kProd][2], drain;       // their copies; products after a failure
+  alignas(16) uint8_t codes[kMaxProd][32 * kCodeBytes];   // of a producer's 32 rows
+  uint64_t drain;                         // products after a failure
   float rk[kKSl][kTT];                    // key scales
   float wv[kVSt][kTT];                    // value scales
   alignas(16) float cs[64], nm[64], cw[64], mp[64];   // (read four at a time) per row: logit scale, -reference of the sum, 2^(sum's - w p's), w p's
@@ -95,22 +94,11 @@ static_assert(offsetof(Sm, cs) % 16 == 0 && offsetof(Sm, nm) % 16 == 0 && offset
               offsetof(Sm, Q) % 1024 == 0, "16-byte reads, swizzle atoms");
 static_assert(kVSt == 2, "the value ring and the P buffers share the barrier pv");
 
-// Four rows (y) of 64 columns from x on, 128 bytes each, swizzled like a tile.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, int y0, int y1, int y2, int y3,
-                                        uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4, %5, %6}], [%7];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// `bytes` (a multiple of 16) from a 16-byte aligned address.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -228,125 +216,131 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {   // byte offset o
   return (uint32_t)((chunk >> 3) * kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-// Work of a producer warp: 32 rows of one tile and side.  Jobs go round the
-// producer warps, which need nothing from one another, four quarters at a
-// time: keys of tile 0, keys 1, values 0, keys 2, values 1, ...  The keys are a
-// tile ahead so that a value job waiting for its stage holds up no logits.
-struct Job {
-  int tile, side, q;                      // tile of this CTA's share, quarter
+// A producer warp fills one quarter (32 rows) of the tiles of one side: warp w
+// has side (w >> 2) & 1, quarter w & 3 and the tiles w >> 3, + step, ...
+struct Lane {
+  int side, q, first, step;
 };
-__device__ __forceinline__ Job job_of(int id) {
-  const int s = id >> 2, v = s > 0 && !(s & 1);
-  return Job{v ? (s >> 1) - 1 : (s + 1) >> 1, v, id & 3};
-}
-__device__ __forceinline__ int job_count(int n) { return 8 * n + 4; }   // among them four of a key tile that is not there
-
-// The job's stage is free: the products that read its last tile are done
-// (keys: the logits, values: the outputs).
-__device__ __forceinline__ uint64_t* stage_free(Sm& sm, const Job& j) {
-  return j.side ? &sm.pv[j.tile & 1] : &sm.kempty[j.tile & 1];
+template <int kProd>
+__device__ __forceinline__ Lane lane_of(int w) {
+  return Lane{(w >> 2) & 1, w & 3, w >> 3, kProd / 8};
 }
 
-__device__ __forceinline__ void job_scales(Sm& sm, const Job& j, int row, float w) {
-  (j.side ? sm.wv[j.tile % kVSt] : sm.rk[j.tile % kKSl])[row] = w;
-}
-__device__ __forceinline__ void job_scales_done(Sm& sm, const Job& j) {
-  tc::mbar_arrive(j.side ? &sm.sv[j.tile % kVSt] : &sm.sk[j.tile % kKSl]);
+// The stage of tile t is free: the products that read it last are done (keys:
+// the logits, values: the outputs).
+__device__ __forceinline__ void wait_free(Sm& sm, int side, int t, const TreeArgs& a) {
+  if (t >= 2) wait_b(sm, side ? &sm.pv[t & 1] : &sm.kempty[t & 1], ((t >> 1) - 1) & 1, a);
 }
 
-// What a job's 32 tokens are, one per lane, as loaded: token word, the tile's
-// bitmap and its first record.
+__device__ __forceinline__ float* scales_of(Sm& sm, int side, int t) { return side ? sm.wv[t % kVSt] : sm.rk[t % kKSl]; }
+__device__ __forceinline__ void scales_done(Sm& sm, int side, int t) {
+  tc::mbar_arrive(side ? &sm.sv[t % kVSt] : &sm.sk[t % kKSl]);
+}
+
+// What a quarter's 32 tokens are, one per lane, as loaded: token word, the
+// tile's bitmap and its first record.
 struct Raw {
   uint32_t word;
   uint4 bm;
   int rec;
 };
-// ... and as used: the bitmap's word and the record of its first bit.
-struct Tok {
-  uint32_t word, bits;
-  int rec;
-};
 
-__device__ __forceinline__ Raw load_tok(const TreeArgs& a, const uint8_t* comp, int h, int tile0, int n, int id) {
-  const Job j = job_of(id);
-  Raw t = {0u, make_uint4(0u, 0u, 0u, 0u), 0};
-  if (j.tile >= n) return t;
-  const int sh = j.side * a.H + h, tile = tile0 + j.tile;
-  const int at = tile * kTT + j.q * 32 + (threadIdx.x & 31);
-  if (at < a.N) t.word = reinterpret_cast<const uint32_t*>(comp + a.off_tok)[(int64_t)sh * a.N + at];
-  t.bm = *reinterpret_cast<const uint4*>(comp + a.off_bm + ((int64_t)sh * a.n_tiles + tile) * 16);
-  t.rec = reinterpret_cast<const int*>(comp + a.off_pf)[(int64_t)sh * (a.n_tiles + 1) + tile];
-  return t;
-}
-
-__device__ __forceinline__ Tok make_tok(const TreeArgs& a, const Raw& r, int tile0, int id) {
-  const Job j = job_of(id);
-  Tok t = {r.word, j.q == 0 ? r.bm.x : j.q == 1 ? r.bm.y : j.q == 2 ? r.bm.z : r.bm.w, r.rec};
-  if (j.q > 0) t.rec += __popc(r.bm.x);
-  if (j.q > 1) t.rec += __popc(r.bm.y);
-  if (j.q > 2) t.rec += __popc(r.bm.z);
-  const int left = a.N - ((tile0 + j.tile) * kTT + j.q * 32);          // bits behind the last token mean nothing
-  if (left < 32) t.bits &= left > 0 ? (1u << left) - 1u : 0u;
-  if (t.rec < 0 || t.rec + (int64_t)__popc(t.bits) > a.R) t.bits = 0u;
-  return t;
-}
-
-__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* comp, int rep, int h, int tile0,
-                               const CUtensorMap* map) {
-  const int lane = threadIdx.x & 31, c = lane & 7, g = lane >> 3;
+template <int kProd>
+__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* comp, int rep, int h, int tile0) {
+  const Lane me = lane_of<kProd>(w);
+  const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4, c8 = lane & 7, g = lane >> 3;
+  const int sh = me.side * a.H + h;
   const __half l0 = __float2half_rn(a.lev[0]), l1 = __float2half_rn(a.lev[1]);
   const __half2 lo = __halves2half2(l0, l1), hi = __halves2half2(__hneg(l1), __hneg(l0));
-  const int64_t row0 = ((int64_t)rep * 2 * a.H + h) * a.k, side_rows = (int64_t)a.H * a.k;
+  const int64_t row0 = ((int64_t)rep * 2 * a.H + sh) * a.k;
+  const uint8_t* rows = reinterpret_cast<const uint8_t*>(a.anc) + row0 * (kD * 2) + c * 16;
+  const float* scale = a.anc_scale + row0;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(comp + a.off_tok) + (int64_t)sh * a.N;
+  const uint4* bms = reinterpret_cast<const uint4*>(comp + a.off_bm) + (int64_t)sh * a.n_tiles;
+  const int* pfs = reinterpret_cast<const int*>(comp + a.off_pf) + (int64_t)sh * (a.n_tiles + 1);
   const uint8_t* codes = comp + a.off_codes;
   const uint16_t* sig = reinterpret_cast<const uint16_t*>(comp + a.off_sig);
-  auto slot_of = [&](const Tok& t) { return min((int)(t.word & 0xffffu), a.k - 1); };
-  auto scale_of = [&](const Tok& t, int id) { return a.anc_scale[row0 + job_of(id).side * side_rows + slot_of(t)]; };
-  auto sigma_of = [&](const Tok& t) {
-    return (t.bits >> lane) & 1u ? half_bits_to_f(sig[t.rec + __popc(t.bits & ((1u << lane) - 1u))]) : 0.f;
-  };
-  // Token words two jobs ahead, what hangs on them one job ahead.  Loaded words
-  // are first looked at a job later, so that no job waits for memory.
-  const Raw r0 = load_tok(a, comp, h, tile0, n, w);
-  Raw r1 = load_tok(a, comp, h, tile0, n, w + kProd);
-  Tok t0 = make_tok(a, r0, tile0, w);
-  float m0 = scale_of(t0, w), s0 = sigma_of(t0);
-  // the job whose copies are in flight: its residual rows, their factors
-  bool pending = false;
-  Job last = {};
-  uint32_t last_bits = 0, last_f = 0;
-  int issued = 0;                         // jobs of this warp: buffer and phase of their copies
+  const uint32_t below = (1u << lane) - 1u, code_buf = tc::smem_u32(sm.codes[w]);
 
-  // completes the last job issued
-  auto finish = [&](int k) {
-    const int buf = k & 1;
-    uint8_t* tile = last.side ? sm.V[last.tile & 1] : sm.K[last.tile & 1];
-    const uint8_t* cd = sm.codes[w][buf] + c * 2;
-    // bounded, and not cut short where another role has failed: the copies
-    // have to be over before this CTA's shared memory is
-    if (!tc::mbar_done(&sm.landed[w][buf], (k >> 1) & 1) && !tc::mbar_wait(&sm.landed[w][buf], (k >> 1) & 1)) {
-      *(volatile int*)&sm.err = 1;
-      latch_error(a.counters, kDevErrTimeout);
+  auto load_raw = [&](int t) {
+    Raw r = {0u, make_uint4(0u, 0u, 0u, 0u), 0};
+    if (t < n) {
+      const int tile = tile0 + t, at = tile * kTT + me.q * 32 + lane;
+      if (at < a.N) r.word = words[at];
+      r.bm = bms[tile];
+      r.rec = pfs[tile];
     }
-    // four records at a time, eight lanes each, two 16-byte pieces a lane
+    return r;
+  };
+  // this quarter's words of a tile: residual bits and the first one's record
+  uint32_t word = 0, bits = 0;
+  int rec = 0;
+  float m = 0.f, sg = 0.f;
+  auto take = [&](const Raw& r, int t) {
+    word = r.word;
+    bits = me.q == 0 ? r.bm.x : me.q == 1 ? r.bm.y : me.q == 2 ? r.bm.z : r.bm.w;
+    rec = r.rec;
+    if (me.q > 0) rec += __popc(r.bm.x);
+    if (me.q > 1) rec += __popc(r.bm.y);
+    if (me.q > 2) rec += __popc(r.bm.z);
+    const int left = a.N - ((tile0 + t) * kTT + me.q * 32);        // bits behind the last token mean nothing
+    if (left < 32) bits &= left > 0 ? (1u << left) - 1u : 0u;
+    if (rec < 0 || rec + (int64_t)__popc(bits) > a.R) bits = 0u;
+    m = scale[min((int)(word & 0xffffu), a.k - 1)];
+    sg = (bits >> lane) & 1u ? half_bits_to_f(sig[rec + __popc(bits & below)]) : 0.f;
+  };
+
+  // token words two tiles ahead, what hangs on them one tile ahead
+  Raw r0 = load_raw(me.first);
+  Raw r1 = load_raw(me.first + me.step);
+  take(r0, me.first);
+  for (int t = me.first; t < n; t += me.step) {
+    // scale of the row; a residual's row keeps the larger of its two factors at 1
+    const float c1 = half_bits_to_f(word >> 16) * m;
+    const float sc = fabsf(c1) >= sg ? c1 : sg;
+    const float inv = sc != 0.f ? __fdividef(1.f, sc) : 0.f;
+    const uint32_t fac = pack_half2(c1 * inv, sg * inv), cur = bits;
+    wait_free(sm, me.side, t, a);
+    scales_of(sm, me.side, t)[me.q * 32 + lane] = sc;             // 0 behind the last token, whose word is 0
+    __syncwarp();
+    if (lane == 0) scales_done(sm, me.side, t);
+    // anchor rows, sixteen lanes each; the residuals' codes as one block
+    uint8_t* tile = (me.side ? sm.V[t & 1] : sm.K[t & 1]) + me.q * 32 * 128;
+    const uint32_t base = tc::smem_u32(tile);
+    const uint32_t slot = min((int)(word & 0xffffu), a.k - 1) * (kD * 2);
+#pragma unroll
+    for (int r = 0; r < 32; r += 2) {
+      const uint32_t s = __shfl_sync(0xffffffffu, slot, r + hw);
+      cp_async16(base + swz(r + hw, c), rows + s);
+    }
+    const uint8_t* cs = codes + (int64_t)rec * kCodeBytes;
+    for (int x = lane; x < 2 * __popc(cur); x += 32) cp_async16(code_buf + x * 16, cs + x * 16);
+    cp_commit();
+    take(r1, t + me.step);
+    r1 = load_raw(t + 2 * me.step);
+    cp_wait();
+    __syncwarp();                                                  // the whole warp's copies have landed
+    // residual rows in place: four records at a time, eight lanes each, two
+    // 16-byte pieces a lane
     int x = g;
-    for (uint32_t m = last_bits; m; x += 4) {
+    for (uint32_t left = cur; left; x += 4) {
       int tk = -1;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (k == g && m) tk = __ffs(m) - 1;
-        m &= m - 1;
+        if (k == g && left) tk = __ffs(left) - 1;
+        left &= left - 1;
       }
-      const uint32_t f = __shfl_sync(0xffffffffu, last_f, max(tk, 0));
+      const uint32_t f = __shfl_sync(0xffffffffu, fac, max(tk, 0));
       if (tk >= 0) {
         const __half2 f2 = *reinterpret_cast<const __half2*>(&f), ca = __low2half2(f2), cb = __high2half2(f2);
         const __half2 tlo = __hmul2(cb, lo), thi = __hmul2(cb, hi);
         const uint32_t t01 = *reinterpret_cast<const uint32_t*>(&tlo), t23 = *reinterpret_cast<const uint32_t*>(&thi);
-        uint8_t* row = tile + swz(last.q * 32 + tk, c);
+        uint8_t* row = tile + swz(tk, c8);
         uint32_t code[2];
         uint4 v[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          code[y] = *reinterpret_cast<const uint16_t*>(cd + x * kCodeBytes + y * 16);
+          code[y] = *reinterpret_cast<const uint16_t*>(sm.codes[w] + x * kCodeBytes + y * 16 + c8 * 2);
           v[y] = *reinterpret_cast<const uint4*>(row + y * kHalf);
         }
 #pragma unroll
@@ -367,76 +361,22 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&sm.full[last.side][last.tile & 1]);
-    pending = false;
-  };
-
-  for (int id = w; id < job_count(n); id += kProd) {
-    const Job j = job_of(id);
-    const Tok t = t0;
-    const float m = m0, sg = s0;
-    t0 = make_tok(a, r1, tile0, id + kProd);
-    r1 = load_tok(a, comp, h, tile0, n, id + 2 * kProd);
-    m0 = scale_of(t0, id + kProd);
-    s0 = sigma_of(t0);
-    // scale of the row; a residual's row keeps the larger of the two factors at 1
-    const bool res = (t.bits >> lane) & 1u;
-    const float c1 = half_bits_to_f(t.word >> 16) * m;
-    float scale = c1, ca = 1.f, cb = 0.f;
-    if (res) {
-      const bool by_anchor = fabsf(c1) >= sg;
-      scale = by_anchor ? c1 : sg;
-      ca = by_anchor ? 1.f : __fdividef(c1, sg);
-      cb = by_anchor ? (c1 != 0.f ? __fdividef(sg, c1) : 0.f) : 1.f;
-    }
-    if (j.tile >= n) continue;
-    if (j.tile >= 2) {
-      uint64_t* bar = stage_free(sm, j);
-      const uint32_t ph = ((j.tile >> 1) - 1) & 1;
-      // the stage is still being read: finish the job before in the meantime
-      if (pending && !__shfl_sync(0xffffffffu, (int)tc::mbar_done(bar, ph), 0)) finish(issued - 1);
-      wait_b(sm, bar, ph, a);
-    }
-    job_scales(sm, j, j.q * 32 + lane, scale);   // 0 behind the last token, whose word is 0
-    __syncwarp();
-    if (lane == 0) job_scales_done(sm, j);
-    // anchor rows by slot, four rows and half their coordinates a copy; the
-    // residuals' codes as one block
-    const uint32_t base = tc::smem_u32(j.side ? sm.V[j.tile & 1] : sm.K[j.tile & 1]);
-    const int row = (int)(row0 + j.side * side_rows) + slot_of(t);
-    int y[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, c * 4 + k);
-    const int parity = issued & 1;
-    const uint32_t bar = tc::smem_u32(&sm.landed[w][parity]), n_codes = kCodeBytes * __popc(t.bits);
-    if (lane == 0) tc::mbar_expect_tx(&sm.landed[w][parity], 32 * kD * 2 + n_codes);
-    __syncwarp();
-    if (lane < 16)
-      gather4(base + g * kHalf + (j.q * 32 + c * 4) * 128, map, g * 64, y[0], y[1], y[2], y[3], bar);
-    if (lane == 16 && n_codes)
-      bulk_copy(tc::smem_u32(sm.codes[w][parity]), codes + (int64_t)t.rec * kCodeBytes, n_codes, bar);
-    if (pending) finish(issued - 1);
-    ++issued;
-    pending = true;
-    last = j;
-    last_bits = t.bits;
-    last_f = pack_half2(ca, cb);
+    if (lane == 0) tc::mbar_arrive(&sm.full[me.side][t & 1]);
   }
-  if (pending) finish(issued - 1);
 }
 
 // Exact rows, of pages and drafts: half a warp per row.
+template <int kProd>
 __device__ void produce_tail(const TreeArgs& a, Sm& sm, int w, int n, int b, int h, int tile0, int len, int n_new) {
+  const Lane me = lane_of<kProd>(w);
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4;
-  for (int id = w; id < job_count(n); id += kProd) {
-    const Job j = job_of(id);
-    if (j.tile >= n) continue;
-    const uint16_t* pool = reinterpret_cast<const uint16_t*>(j.side ? a.vp : a.kp);
-    const uint16_t* fresh = reinterpret_cast<const uint16_t*>(j.side ? a.vn : a.kn);
-    if (j.tile >= 2) wait_b(sm, stage_free(sm, j), ((j.tile >> 1) - 1) & 1, a);
-    uint8_t* tile = j.side ? sm.V[j.tile & 1] : sm.K[j.tile & 1];
-    const int first = (tile0 + j.tile) * kTT;
-    for (int r0 = j.q * 32 + hw; r0 < j.q * 32 + 32; r0 += 8) {
+  const uint16_t* pool = reinterpret_cast<const uint16_t*>(me.side ? a.vp : a.kp);
+  const uint16_t* fresh = reinterpret_cast<const uint16_t*>(me.side ? a.vn : a.kn);
+  for (int tl = me.first; tl < n; tl += me.step) {
+    wait_free(sm, me.side, tl, a);
+    uint8_t* tile = me.side ? sm.V[tl & 1] : sm.K[tl & 1];
+    const int first = (tile0 + tl) * kTT;
+    for (int r0 = me.q * 32 + hw; r0 < me.q * 32 + 32; r0 += 8) {
       uint4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -472,7 +412,7 @@ __device__ void produce_tail(const TreeArgs& a, Sm& sm, int w, int n, int b, int
           odd = odd || !fin;
           // an infinity or NaN in a draft's value must not reach the rows that
           // do not see it (0 x inf): the merge adds it where it is seen
-          if (!fin && j.side && t >= len) x[y] = 0.f;
+          if (!fin && me.side && t >= len) x[y] = 0.f;
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -481,15 +421,15 @@ __device__ void produce_tail(const TreeArgs& a, Sm& sm, int w, int n, int b, int
         *reinterpret_cast<uint4*>(tile + swz(r, c)) =
             make_uint4(pack_half2(x[0] * inv, x[1] * inv), pack_half2(x[2] * inv, x[3] * inv),
                        pack_half2(x[4] * inv, x[5] * inv), pack_half2(x[6] * inv, x[7] * inv));
-        if (odd && j.side && t >= len) atomicOr(&a.inf_v[(int64_t)b * a.H + h], 1ull << (t - len));
-        if (c == 0) job_scales(sm, j, r, m ? exp_to_f(e) : (j.side ? 0.f : 1.f));
+        if (odd && me.side && t >= len) atomicOr(&a.inf_v[(int64_t)b * a.H + h], 1ull << (t - len));
+        if (c == 0) scales_of(sm, me.side, tl)[r] = m ? exp_to_f(e) : (me.side ? 0.f : 1.f);
       }
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      job_scales_done(sm, j);
-      tc::mbar_arrive(&sm.full[j.side][j.tile & 1]);
+      scales_done(sm, me.side, tl);
+      tc::mbar_arrive(&sm.full[me.side][tl & 1]);
     }
   }
 }
@@ -504,12 +444,12 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&v)[16]) {
 // warps that share them.
 template <int NC>
 struct Shape {
-  static constexpr int SW = NC == 64 ? 2 : 1, CW = NC / SW;
+  static constexpr int SW = NC == 64 ? 2 : 1, CW = NC / SW, kProd = NC == 64 ? 8 : 16;
   static constexpr int kMma = 4 * SW, kFirstProd = kMma + 1, kThreads = 32 * (kFirstProd + kProd);
 };
 
 template <int NC>
-__global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArgs a) {
   constexpr int SW = Shape<NC>::SW, CW = Shape<NC>::CW, kMma = Shape<NC>::kMma, kThreads = Shape<NC>::kThreads;
   extern __shared__ __align__(1024) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -548,7 +488,6 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   if (tid == 0) {
     for (int i = 0; i < kKSl; ++i) tc::mbar_init(&sm.sk[i], 4);          // four quarters of a tile
     for (int i = 0; i < kVSt; ++i) tc::mbar_init(&sm.sv[i], 4);
-    for (int i = 0; i < 2 * kProd; ++i) tc::mbar_init(&sm.landed[0][0] + i, 1);
     tc::mbar_init(&sm.drain, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.full[0][i], 4);
@@ -652,8 +591,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   } else if (warp > kMma) {
     // ---- rows of the key and value tiles
     const int w = warp - Shape<NC>::kFirstProd;
-    if (tail) produce_tail(a, sm, w, n, b, h, tile0, len, n_new);
-    else produce_prefix(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0, &map);
+    if (tail) produce_tail<Shape<NC>::kProd>(a, sm, w, n, b, h, tile0, len, n_new);
+    else produce_prefix<Shape<NC>::kProd>(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0);
   } else {
     // ---- softmax: thread = token, a group of four warps has CW of the rows
     const int tok = tid & 127, wq = warp & 3, c0 = (warp >> 2) * CW, bar_id = 1 + (warp >> 2);
@@ -902,24 +841,6 @@ int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t s,
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ANCHORKV_OK : ANCHORKV_ECUDA;
 }
 
-// The rotated anchors as rows of D fp16, gathered four rows and 64 columns at
-// a time (a gather's box is one row high).
-bool anchor_map(CUtensorMap* m, const void* base, int64_t rows) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-  }();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {kD, (cuuint64_t)rows}, strides[1] = {kD * 2};
-  const cuuint32_t box[2] = {64, 1}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr int kSmem = (int)sizeof(Sm) + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 
@@ -937,12 +858,10 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
       ready_dev = dev;
     }
   }
-  CUtensorMap map;
-  if (!anchor_map(&map, a.anc, (int64_t)a.batch * 2 * a.H * a.k)) return ANCHORKV_ECUDA;
   const int gx = a.comp ? std::max(1, std::min((a.k + 7) / 8, 256)) : 1;
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  int st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, s, a, map);
+  int st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, s, a);
   if (st) return st;
   const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
   return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 7) / 8)), 256, 0, s, a);
