@@ -28,8 +28,8 @@
 // Tokens are on the accumulator's lanes, so a thread owns a token: its scales
 // are scalars, its row of P is contiguous, and the cost of the softmax goes
 // with the rows there are (16, 32 or 64 columns) instead of a padded 128.
-//   softmax, 4 warps for 16 or 32 rows and 8 for 64: logits from tensor
-//     memory, exponentials, P to shared memory; at the end the outputs
+//   softmax, 8 warps (16 for 64 rows): logits from tensor memory, exponentials,
+//     P to shared memory; at the end the outputs
 //   one warp issues the MMAs
 //   16 or 8 warps fill key and value tiles, 32 rows each: anchor rows by
 //     16-byte asynchronous copies into the 128-byte swizzle, residual rows
@@ -60,13 +60,15 @@ constexpr int kKSt = 2, kVSt = 2;         // stages of the key and value rings
 constexpr int kKSl = kKSt + 2;            // key scales outlive their tile by the two logit buffers
 constexpr int kTileBytes = kTT * kD * 2;
 constexpr int kHalf = kTileBytes / 2;     // 64 coordinates of every row
-constexpr int kOCols = 64;                // output columns in tensor memory
+constexpr int kOCols = 64;                // output columns in tensor memory, twice (even and odd tiles)
+constexpr int kSCol = 2 * kOCols;         // logits
 constexpr int kTmemCols = 256;
 constexpr float kLog2e = 1.4426950408889634f;
-// A new reference puts the largest |w p| between 1/2 and 1: 2^15 above it for
-// later tiles, and what fp16 rounds away below 2^-14 is at most 2^-25 of the
-// largest contribution each.
+// A new reference puts the largest |w p| between 2^-6 and 2^-5: 20 bits below
+// the limit for later tiles, and what fp16 rounds away below 2^-14 is at most
+// 2^-19 of the largest contribution each.
 constexpr float kPLimit = 32768.f;        // fp16 holds 65504
+constexpr float kPTarget = 5.f;
 constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
 constexpr float kRefGap = 120.f;          // the references' largest distance downwards
 
@@ -79,10 +81,13 @@ struct Sm {
   uint64_t drain;                         // products after a failure
   float rk[kKSl][kTT];                    // key scales
   float wv[kVSt][kTT];                    // value scales
-  alignas(16) float cs[64], nm[64], cw[64], mp[64];   // (read four at a time) per row: logit scale, -reference of the sum, 2^(sum's - w p's), w p's
-  float fl[64], fp[64];                   // rescaling factors
-  int red[2][4][64];
-  float lsum[4][64];
+  alignas(16) float cs[64];               // per row: logit scale
+  // per row, of the even and the odd tiles: -reference of the sum,
+  // 2^(reference of the sum - that of w p), reference of w p
+  alignas(16) float nm[2][64], cw[2][64], mp[2][64];
+  float fl[2][64];                        // rescaling of the sums
+  int red[2][2][4][64];
+  float lsum[2][4][64];
   unsigned long long mask[kTreeMaxDrafts];
   unsigned char colt[64];                 // draft of each row
   uint64_t full[2][2], kempty[kKSt], pv[2], sfull[2], sempty[2], pfull[2], sk[kKSl], sv[kVSt];   // full: [side][stage]
@@ -131,12 +136,10 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -152,6 +155,20 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
+}
+
+// One MMA of fp16 operands whose descriptors differ from a tile's first only in
+// their low words.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint32_t a_off, uint64_t b, uint32_t b_off, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}"
+      ::"r"(d), "r"((uint32_t)a + (a_off >> 4)), "r"((uint32_t)(a >> 32)), "r"((uint32_t)b + (b_off >> 4)),
+        "r"((uint32_t)(b >> 32)), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
 }
 
 // First sequence with the layout of sequence b: it holds the rotated anchors.
@@ -440,17 +457,92 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&v)[16]) {
   tc::tmem_wait_ld_dep(v);
 }
 
-// NC: rows (columns of the accumulators) of a CTA, SW: groups of four softmax
-// warps that share them.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&a)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7])
+               :
+               : "memory");
+}
+// New references of rows c1 .. c1 + 15 for a softmax group whose last tile was
+// `before` (negative: none): the maxima over the tile's tokens, the factor of the sums so far (fl), and the
+// outputs so far in tensor memory.  Out of line and in loops: it runs once or
+// twice, and its code should not push the tile loops out of the instruction
+// caches.
+__device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t scol, uint32_t ocol, int c1, int par,
+                                            int before, int bar_id, float rk, float w, unsigned long long vis) {
+  const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, tok = threadIdx.x & 127;
+  const float lw = w != 0.f ? __log2f(fabsf(w)) : -INFINITY;
+#pragma unroll 1
+  for (int x = 0; x < 16; x += 8) {
+    uint32_t s[8];
+    tmem_ld8(scol + x, s);
+    tmem_wait_ld8(s);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const int c = c1 + x + y;
+      float lg = (vis >> sm.colt[c]) & 1ull ? __uint_as_float(s[y]) * (rk * sm.cs[c]) : -INFINITY;
+      lg = fmaxf(lg, -INFINITY);                                   // a NaN is no maximum
+      const int m1 = __reduce_max_sync(0xffffffffu, ordered(lg));
+      const int m2 = __reduce_max_sync(0xffffffffu, ordered(lg + lw));
+      if (lane == 0) {
+        sm.red[par][0][wq][c] = m1;
+        sm.red[par][1][wq][c] = m2;
+      }
+    }
+  }
+  tc::named_bar(bar_id, 128);
+  float* factor = reinterpret_cast<float*>(sm.red[par][0][0]) + c1;       // of the outputs, once the maxima are read
+  if (tok < 16) {
+    const int c = c1 + tok;
+    const int(&r)[2][4][64] = sm.red[par];
+    const float m1 = unordered(max(max(r[0][0][c], r[0][1][c]), max(r[0][2][c], r[0][3][c])));
+    const float m2 = unordered(max(max(r[1][0][c], r[1][1][c]), max(r[1][2][c], r[1][3][c])));
+    const float l_old = -sm.nm[par][c], p_old = sm.mp[par][c];
+    const float l_new = fmaxf(l_old, ceilf(m1));
+    float p_new = fmaxf(p_old, ceilf(m2) + kPTarget);
+    if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
+    sm.fl[par][c] = l_old > -INFINITY ? exp2f(l_old - l_new) : 0.f;
+    sm.nm[par][c] = -l_new;
+    sm.mp[par][c] = p_new;
+    sm.cw[par][c] = l_new > -INFINITY ? exp2f(l_new - p_new) : 1.f;
+    __syncwarp(0xffffu);
+    factor[tok] = p_old > -INFINITY ? exp2f(p_old - p_new) : 0.f;
+  }
+  tc::named_bar(bar_id, 128);
+  if (before >= 0) {
+    wait_b(sm, &sm.pv[before & 1], (before >> 1) & 1, a);
+    tc::fence_after_sync();
+#pragma unroll 1
+    for (int x = 0; x < 16; x += 8) {
+      uint32_t o[8];
+      tmem_ld8(ocol + x, o);
+      tmem_wait_ld8(o);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * factor[x + y]);
+      tmem_st8(ocol + x, o);
+    }
+    tmem_wait_st();
+  }
+}
+
+// NC: rows (columns of the accumulators) of a CTA.  Softmax groups of four
+// warps have 16 of the rows each, and every tile or (PG = 2) every other tile;
+// then the warp that issues the MMAs, then the producers.
 template <int NC>
 struct Shape {
-  static constexpr int SW = NC == 64 ? 2 : 1, CW = NC / SW, kProd = NC == 64 ? 8 : 16;
-  static constexpr int kMma = 4 * SW, kFirstProd = kMma + 1, kThreads = 32 * (kFirstProd + kProd);
+  static constexpr int CG = NC / 16, PG = NC == 16 ? 2 : 1, kProd = NC == 64 ? 8 : 16;
+  static constexpr int kMma = 4 * CG * PG, kFirstProd = kMma + 1, kThreads = 32 * (kFirstProd + kProd);
 };
 
 template <int NC>
 __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArgs a) {
-  constexpr int SW = Shape<NC>::SW, CW = Shape<NC>::CW, kMma = Shape<NC>::kMma, kThreads = Shape<NC>::kThreads;
+  constexpr int CG = Shape<NC>::CG, PG = Shape<NC>::PG, kMma = Shape<NC>::kMma, kThreads = Shape<NC>::kThreads;
   extern __shared__ __align__(1024) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -495,8 +587,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       tc::mbar_init(&sm.kempty[i], 1);
       tc::mbar_init(&sm.pv[i], 1);
       tc::mbar_init(&sm.sfull[i], 1);
-      tc::mbar_init(&sm.sempty[i], 4 * SW);                              // one arrival a warp
-      tc::mbar_init(&sm.pfull[i], 4 * SW);
+      tc::mbar_init(&sm.sempty[i], 4 * CG);                              // one arrival a warp
+      tc::mbar_init(&sm.pfull[i], 4 * CG);
     }
     tc::fence_barrier_init();
     sm.err = 0;
@@ -506,9 +598,11 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   if (tid < 64) {
     const int r = blk * NC + tid;
     sm.colt[tid] = (unsigned char)min(r / a.G, a.T - 1);
-    sm.nm[tid] = INFINITY;
-    sm.mp[tid] = -INFINITY;
-    sm.cw[tid] = 1.f;
+    for (int i = 0; i < 2; ++i) {
+      sm.nm[i][tid] = INFINITY;
+      sm.mp[i][tid] = -INFINITY;
+      sm.cw[i][tid] = 1.f;
+    }
     if (tid < a.T) sm.mask[tid] = tree_mask(a, b, tid);
   }
   if (NC < kOCols)                                    // columns of P that no row fills
@@ -545,39 +639,44 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = sm.tmem;
 
-  if (warp == kMma) {
-    // ---- MMA issue
+  if (warp >= Shape<NC>::kFirstProd) {
+    // ---- rows of the key and value tiles
+    const int w = warp - Shape<NC>::kFirstProd;
+    if (tail) produce_tail<Shape<NC>::kProd>(a, sm, w, n, b, h, tile0, len, n_new);
+    else produce_prefix<Shape<NC>::kProd>(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0);
+  } else if (warp == kMma) {
     {
+      // ---- MMA issue
       const bool one = elect_one();
       constexpr uint32_t id_s = idesc_f16(128, NC, 0, 0), id_o = idesc_f16(128, kOCols, 1, 1);
-      const uint32_t kb = tc::smem_u32(sm.K), vb = tc::smem_u32(sm.V), pb = tc::smem_u32(sm.P), qb = tc::smem_u32(sm.Q);
+      const uint64_t kd = tc::sw128_desc(tc::smem_u32(sm.K)), qd = tc::sw128_desc(tc::smem_u32(sm.Q));
+      const uint64_t vd = tc::sw128_mn_desc(tc::smem_u32(sm.V), kHalf), pd = tc::sw128_mn_desc(tc::smem_u32(sm.P), kTT * 128);
       for (int i = 0; i <= n; ++i) {
+        const int bf = i & 1;
         if (i < n) {
-          const int st = i % kKSt, bf = i & 1;
-          wait_b(sm, &sm.full[0][st], (i / kKSt) & 1, a);
+          wait_b(sm, &sm.full[0][bf], (i >> 1) & 1, a);
           if (i >= 2) wait_b(sm, &sm.sempty[bf], ((i >> 1) - 1) & 1, a);
           tc::fence_after_sync();
           if (one && !*(volatile int*)&sm.err) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              tc::mma_bf16(tmem + kOCols + bf * NC,
-                           tc::sw128_desc(kb + st * kTileBytes + (ks >> 2) * kHalf + (ks & 3) * 32),
-                           tc::sw128_desc(qb + (ks >> 2) * (NC * 128) + (ks & 3) * 32), id_s, ks > 0);
-            tc::mma_commit(&sm.kempty[st]);
+              mma_f16(tmem + kSCol + bf * NC, kd, bf * kTileBytes + (ks >> 2) * kHalf + (ks & 3) * 32, qd,
+                      (ks >> 2) * (NC * 128) + (ks & 3) * 32, id_s, ks > 0);
+            tc::mma_commit(&sm.kempty[bf]);
             tc::mma_commit(&sm.sfull[bf]);
           }
         }
         if (i > 0) {
-          const int o = i - 1, st = o % kVSt;
-          wait_b(sm, &sm.full[1][st], (o / kVSt) & 1, a);
-          wait_b(sm, &sm.pfull[o & 1], (o >> 1) & 1, a);
+          const int o = i - 1, ob = o & 1;
+          wait_b(sm, &sm.full[1][ob], (o >> 1) & 1, a);
+          wait_b(sm, &sm.pfull[ob], (o >> 1) & 1, a);
           tc::fence_after_sync();
           if (one && !*(volatile int*)&sm.err) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              tc::mma_bf16(tmem, tc::sw128_mn_desc(vb + st * kTileBytes + ks * 2048, kHalf),
-                           tc::sw128_mn_desc(pb + (o & 1) * (kTT * 128) + ks * 2048, kTT * 128), id_o, o > 0 || ks > 0);
-            tc::mma_commit(&sm.pv[o & 1]);
+              mma_f16(tmem + (PG == 2 ? ob * kOCols : 0), vd, ob * kTileBytes + ks * 2048, pd, ob * (kTT * 128) + ks * 2048,
+                      id_o, o >= PG || ks > 0);
+            tc::mma_commit(&sm.pv[ob]);
           }
         }
       }
@@ -586,21 +685,19 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         if (one) tc::mma_commit(&sm.drain);
         tc::mbar_wait(&sm.drain, 0);
       }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp > kMma) {
-    // ---- rows of the key and value tiles
-    const int w = warp - Shape<NC>::kFirstProd;
-    if (tail) produce_tail<Shape<NC>::kProd>(a, sm, w, n, b, h, tile0, len, n_new);
-    else produce_prefix<Shape<NC>::kProd>(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0);
   } else {
-    // ---- softmax: thread = token, a group of four warps has CW of the rows
-    const int tok = tid & 127, wq = warp & 3, c0 = (warp >> 2) * CW, bar_id = 1 + (warp >> 2);
-    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-    float2 lacc[CW / 2];
+    // ---- softmax: thread = token; a group of four warps has 16 of the rows and,
+    // where two groups share them, every other tile with references, sums and
+    // outputs of its own (par)
+    const int tok = tid & 127, wq = warp & 3, grp = warp >> 2, par = PG == 2 ? grp & 1 : 0;
+    const int c0 = 16 * (grp / PG), bar_id = 1 + grp;
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16, ocol = tmem + lane_base + par * kOCols + c0;
+    float2 lacc[8];
 #pragma unroll
-    for (int x = 0; x < CW / 2; ++x) lacc[x] = make_float2(0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
+    for (int x = 0; x < 8; ++x) lacc[x] = make_float2(0.f, 0.f);
+    for (int i = par; i < n; i += PG) {
       const int bf = i & 1;
       // what this token is, and who sees it
       const int t = (tile0 + i) * kTT + tok;
@@ -619,108 +716,57 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       }
       if (!live) vis = 0;
       wait_b(sm, &sm.sk[i % kKSl], (i / kKSl) & 1, a);
-      wait_b(sm, &sm.sv[i % kVSt], (i / kVSt) & 1, a);
-      const float rk = sm.rk[i % kKSl][tok], w = sm.wv[i % kVSt][tok];
+      wait_b(sm, &sm.sv[bf], (i >> 1) & 1, a);
+      const float rk = sm.rk[i % kKSl][tok], w = sm.wv[bf][tok];
       wait_b(sm, &sm.sfull[bf], (i >> 1) & 1, a);
       tc::fence_after_sync();
-      const uint32_t scol = tmem + lane_base + kOCols + bf * NC + c0;
-      uint8_t* prow = sm.P[bf] + tok * 128;
-      float2 p[CW / 2];
-      uint32_t pk[CW / 2];
-      auto exponentials = [&]() {
+      const uint32_t scol = tmem + lane_base + kSCol + bf * NC + c0;
+      float2 p[8];
+      uint32_t pk[8];
+      for (bool again = false;; again = true) {
         float pmax = 0.f, vmax = 0.f;
+        uint32_t s[16];
+        load_cols(scol, s);
 #pragma unroll
-        for (int x = 0; x < CW; x += 16) {
-          uint32_t s[16];
-          load_cols(scol + x, s);
+        for (int y = 0; y < 16; y += 4) {
+          const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c0 + y]);
+          const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[par][c0 + y]);
+          const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[par][c0 + y]);
 #pragma unroll
-          for (int y = 0; y < 16; y += 4) {
-            const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c0 + x + y]);
-            const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[c0 + x + y]);
-            const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[c0 + x + y]);
-#pragma unroll
-            for (int z = 0; z < 4; z += 2) {
-              const float2 k2 = __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk));
-              float2 u = __ffma2_rn(make_float2(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 1])), k2,
-                                    z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
-              if (special) {
-                if (!((vis >> sm.colt[c0 + x + y + z]) & 1ull)) u.x = -INFINITY;
-                if (!((vis >> sm.colt[c0 + x + y + z + 1]) & 1ull)) u.y = -INFINITY;
-              }
-              const float2 e = make_float2(tc::ex2_approx(u.x), tc::ex2_approx(u.y));
-              // in this order a masked 0 stays 0 whatever the value's scale
-              const float2 v = __fmul2_rn(__fmul2_rn(e, make_float2(w, w)),
-                                          z ? make_float2(cw.z, cw.w) : make_float2(cw.x, cw.y));
-              pmax = fmaxf(pmax, fmaxf(e.x, e.y));
-              vmax = fmaxf(vmax, fmaxf(fabsf(v.x), fabsf(v.y)));
-              p[(x + y + z) / 2] = e;
-              pk[(x + y + z) / 2] = pack_half2(v.x, v.y);
+          for (int z = 0; z < 4; z += 2) {
+            const float2 k2 = __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk));
+            float2 u = __ffma2_rn(make_float2(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 1])), k2,
+                                  z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
+            if (special) {
+              if (!((vis >> sm.colt[c0 + y + z]) & 1ull)) u.x = -INFINITY;
+              if (!((vis >> sm.colt[c0 + y + z + 1]) & 1ull)) u.y = -INFINITY;
             }
+            const float2 e = make_float2(tc::ex2_approx(u.x), tc::ex2_approx(u.y));
+            // in this order a masked 0 stays 0 whatever the value's scale
+            const float2 v = __fmul2_rn(__fmul2_rn(e, make_float2(w, w)),
+                                        z ? make_float2(cw.z, cw.w) : make_float2(cw.x, cw.y));
+            pmax = fmaxf(pmax, fmaxf(e.x, e.y));
+            vmax = fmaxf(vmax, fmaxf(fabsf(v.x), fabsf(v.y)));
+            p[(y + z) / 2] = e;
+            pk[(y + z) / 2] = pack_half2(v.x, v.y);
           }
         }
-        return pmax > kSumLimit || vmax > kPLimit;
-      };
-      if (bar_or(bar_id, 128, exponentials())) {
-        // ---- new references for these rows (the first tile, and rarely after)
-        const float lw = w != 0.f ? __log2f(fabsf(w)) : -INFINITY;
-#pragma unroll 1
-        for (int x = 0; x < CW; x += 16) {
-          uint32_t s[16];
-          load_cols(scol + x, s);
+        // a second time only where infinities leave no reference
+        if (!bar_or(bar_id, 128, pmax > kSumLimit || vmax > kPLimit) || again) break;
+        // the first tile, and rarely after: new references for these rows
+        new_references(sm, a, scol, ocol, c0, par, i - PG, bar_id, rk, w, special ? vis : ~0ull);
 #pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            const int c = c0 + x + y;
-            const bool seen = !special || ((vis >> sm.colt[c]) & 1ull);
-            const float lg = seen ? __uint_as_float(s[y]) * (rk * sm.cs[c]) : -INFINITY;
-            const int m1 = __reduce_max_sync(0xffffffffu, ordered(lg));
-            const int m2 = __reduce_max_sync(0xffffffffu, ordered(lg + lw));
-            if (lane == 0) {
-              sm.red[0][wq][c] = m1;
-              sm.red[1][wq][c] = m2;
-            }
-          }
+        for (int x = 0; x < 8; ++x) {
+          lacc[x].x *= sm.fl[par][c0 + 2 * x];
+          lacc[x].y *= sm.fl[par][c0 + 2 * x + 1];
         }
-        tc::named_bar(bar_id, 128);
-        if (tok < CW) {
-          const int c = c0 + tok;
-          const float m1 = unordered(max(max(sm.red[0][0][c], sm.red[0][1][c]), max(sm.red[0][2][c], sm.red[0][3][c])));
-          const float m2 = unordered(max(max(sm.red[1][0][c], sm.red[1][1][c]), max(sm.red[1][2][c], sm.red[1][3][c])));
-          const float l_old = -sm.nm[c], p_old = sm.mp[c];
-          const float l_new = fmaxf(l_old, ceilf(m1));
-          float p_new = fmaxf(p_old, ceilf(m2));
-          if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
-          sm.fl[c] = l_old > -INFINITY ? exp2f(l_old - l_new) : 0.f;
-          sm.fp[c] = p_old > -INFINITY ? exp2f(p_old - p_new) : 0.f;
-          sm.nm[c] = -l_new;
-          sm.mp[c] = p_new;
-          sm.cw[c] = l_new > -INFINITY ? exp2f(l_new - p_new) : 1.f;
-        }
-        tc::named_bar(bar_id, 128);
-#pragma unroll
-        for (int x = 0; x < CW / 2; ++x) {
-          lacc[x].x *= sm.fl[c0 + 2 * x];
-          lacc[x].y *= sm.fl[c0 + 2 * x + 1];
-        }
-        if (i > 0) {
-          wait_b(sm, &sm.pv[(i - 1) & 1], ((i - 1) >> 1) & 1, a);
-          tc::fence_after_sync();
-#pragma unroll 1
-          for (int x = 0; x < CW; x += 16) {
-            uint32_t o[16];
-            load_cols(tmem + lane_base + c0 + x, o);
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * sm.fp[c0 + x + y]);
-            tmem_st16(tmem + lane_base + c0 + x, o);
-          }
-          tmem_wait_st();
-        }
-        exponentials();
       }
 #pragma unroll
-      for (int x = 0; x < CW / 2; ++x) lacc[x] = __fadd2_rn(lacc[x], p[x]);
-      if (i >= 2) wait_b(sm, &sm.pv[bf], ((i >> 1) - 1) & 1, a);   // the outputs that read this buffer of P
+      for (int x = 0; x < 8; ++x) lacc[x] = __fadd2_rn(lacc[x], p[x]);
+      if (i >= 2) wait_b(sm, &sm.pv[bf], ((i >> 1) - 1) & 1, a);   // the products that read this buffer of P
+      uint8_t* prow = sm.P[bf] + tok * 128;
 #pragma unroll
-      for (int x = 0; x < CW / 8; ++x)
+      for (int x = 0; x < 2; ++x)
         *reinterpret_cast<uint4*>(prow + (((c0 / 8 + x) ^ (tok & 7)) << 4)) =
             make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
       tc::fence_proxy_async_smem();
@@ -732,31 +778,63 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // ---- sums over the tokens, outputs in units of the sums' references
+    // ---- sums over the tokens
     {
-      float v[32];
+      float v[16];
 #pragma unroll
-      for (int x = 0; x < 32; ++x) v[x] = x < CW ? (x & 1 ? lacc[(x < CW ? x : 0) / 2].y : lacc[(x < CW ? x : 0) / 2].x) : 0.f;
-      transpose_reduce32(v, lane);
-      if (lane < CW) sm.lsum[wq][c0 + lane] = v[0];
+      for (int x = 0; x < 16; ++x) v[x] = x & 1 ? lacc[x / 2].y : lacc[x / 2].x;
+#pragma unroll
+      for (int off = 8; off >= 1; off >>= 1) {       // lane l ends with column l % 16
+        const bool up = (lane & off) != 0;
+#pragma unroll
+        for (int x = 0; x < off; ++x) {
+          const float keep = up ? v[x + off] : v[x], send = up ? v[x] : v[x + off];
+          v[x] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+      }
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+      if (lane < 16) sm.lsum[par][wq][c0 + lane] = v[0];
     }
-    tc::named_bar(bar_id, 128);
+    // outputs in units of the sum's reference (of the larger, where two groups
+    // have these rows; each writes half of them)
+    tc::named_bar(8 + grp / PG, 128 * PG);
+    if (n > 1) wait_b(sm, &sm.pv[(n - 2) & 1], ((n - 2) >> 1) & 1, a);
     wait_b(sm, &sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, a);
     tc::fence_after_sync();
     const bool nan = *(volatile int*)&sm.err || *(volatile int*)&sm.bad;
     if (nan && tid == 0) latch_error(a.counters, kDevErrBounds);
-    if (tok < CW) {
-      const int c = c0 + tok;
-      ml[2 * c] = nan ? 0.f : -sm.nm[c];
-      ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : sm.lsum[0][c] + sm.lsum[1][c] + sm.lsum[2][c] + sm.lsum[3][c];
-    }
-    float* o = a.part + ((unit * a.parts + part) * NC + c0) * kD + tok;
+    float* o = a.part + (unit * a.parts + part) * NC * kD + tok;
 #pragma unroll 1
-    for (int x = 0; x < CW; x += 16) {
-      uint32_t v[16];
-      load_cols(tmem + lane_base + c0 + x, v);
+    for (int x = c0 + par * (16 / PG); x < c0 + (par + 1) * (16 / PG); x += 8) {
+      uint32_t v[PG][8];
 #pragma unroll
-      for (int y = 0; y < 16; ++y) o[(x + y) * kD] = __uint_as_float(v[y]) * exp2f(sm.mp[c0 + x + y] + sm.nm[c0 + x + y]);
+      for (int k = 0; k < PG; ++k) {
+        tmem_ld8(tmem + lane_base + k * kOCols + x, v[k]);
+        tmem_wait_ld8(v[k]);
+      }
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const int c = x + y;
+        const float m = PG == 2 ? fmaxf(-sm.nm[0][c], -sm.nm[1][c]) : -sm.nm[0][c];
+        float acc = 0.f;
+#pragma unroll
+        for (int k = 0; k < PG; ++k)
+          if (sm.nm[k][c] < INFINITY) acc = fmaf(__uint_as_float(v[k][y]), exp2f(sm.mp[k][c] - m), acc);
+        o[c * kD] = acc;
+      }
+    }
+    if (par == 0 && tok < 16) {
+      const int c = c0 + tok;
+      const float m = PG == 2 ? fmaxf(-sm.nm[0][c], -sm.nm[1][c]) : -sm.nm[0][c];
+      float l = 0.f;
+#pragma unroll
+      for (int k = 0; k < PG; ++k) {
+        const float sum = sm.lsum[k][0][c] + sm.lsum[k][1][c] + sm.lsum[k][2][c] + sm.lsum[k][3][c];
+        // a sum without a reference is zero, or NaN
+        l += sm.nm[k][c] < INFINITY ? sum * exp2f(-sm.nm[k][c] - m) : sum;
+      }
+      ml[2 * c] = nan ? 0.f : m;
+      ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : l;
     }
     tc::fence_before_sync();
   }
