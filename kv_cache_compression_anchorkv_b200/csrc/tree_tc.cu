@@ -78,6 +78,8 @@ struct Sm {
   uint8_t P[2][kTT * 128];                // [token][64 rows] fp16, swizzled
   uint8_t Q[64 * kD * 2];
   alignas(16) uint8_t codes[kMaxProd][32 * kCodeBytes];   // of a producer's 32 rows
+  uint2 ent[kMaxProd][32];                // their residual records: factors, row
+  uint2 lut[256];                         // code byte -> its four levels in fp16
   uint64_t drain;                         // products after a failure
   float rk[kKSl][kTT];                    // key scales
   float wv[kVSt][kTT];                    // value scales
@@ -262,15 +264,21 @@ struct Raw {
   int rec;
 };
 
+// x = ca x + cb level, two coordinates.
+__device__ __forceinline__ void add_levels(uint32_t& x, __half2 ca, __half2 cb, uint32_t level) {
+  const __half2 r = __hfma2(cb, *reinterpret_cast<const __half2*>(&level), __hmul2(ca, *reinterpret_cast<const __half2*>(&x)));
+  x = *reinterpret_cast<const uint32_t*>(&r);
+}
+// Where piece c (of the first half) of the row at byte offset `row` lies in it.
+__device__ __forceinline__ uint32_t c_swz(uint32_t row, int c) { return (uint32_t)(c ^ (int)((row >> 7) & 7u)) << 4; }
+
 template <int kProd>
 __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* comp, int rep, int h, int tile0) {
   const Lane me = lane_of<kProd>(w);
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4, c8 = lane & 7, g = lane >> 3;
   const int sh = me.side * a.H + h;
-  const __half l0 = __float2half_rn(a.lev[0]), l1 = __float2half_rn(a.lev[1]);
-  const __half2 lo = __halves2half2(l0, l1), hi = __halves2half2(__hneg(l1), __hneg(l0));
   const int64_t row0 = ((int64_t)rep * 2 * a.H + sh) * a.k;
-  const uint8_t* rows = reinterpret_cast<const uint8_t*>(a.anc) + row0 * (kD * 2) + c * 16;
+  const uint8_t* rows = reinterpret_cast<const uint8_t*>(a.anc) + row0 * (kD * 2);
   const float* scale = a.anc_scale + row0;
   const uint32_t* words = reinterpret_cast<const uint32_t*>(comp + a.off_tok) + (int64_t)sh * a.N;
   const uint4* bms = reinterpret_cast<const uint4*>(comp + a.off_bm) + (int64_t)sh * a.n_tiles;
@@ -316,22 +324,24 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
     const float c1 = half_bits_to_f(word >> 16) * m;
     const float sc = fabsf(c1) >= sg ? c1 : sg;
     const float inv = sc != 0.f ? __fdividef(1.f, sc) : 0.f;
-    const uint32_t fac = pack_half2(c1 * inv, sg * inv), cur = bits;
+    const int n_rec = __popc(bits);
     wait_free(sm, me.side, t, a);
     scales_of(sm, me.side, t)[me.q * 32 + lane] = sc;             // 0 behind the last token, whose word is 0
     __syncwarp();
     if (lane == 0) scales_done(sm, me.side, t);
+    if ((bits >> lane) & 1u)
+      sm.ent[w][__popc(bits & below)] = make_uint2(pack_half2(c1 * inv, sg * inv), (uint32_t)lane * 128u);
     // anchor rows, sixteen lanes each; the residuals' codes as one block
     uint8_t* tile = (me.side ? sm.V[t & 1] : sm.K[t & 1]) + me.q * 32 * 128;
     const uint32_t base = tc::smem_u32(tile);
-    const uint32_t slot = min((int)(word & 0xffffu), a.k - 1) * (kD * 2);
+    const uint32_t slot = (uint32_t)min((int)(word & 0xffffu), a.k - 1) * (kD * 2);
 #pragma unroll
     for (int r = 0; r < 32; r += 2) {
       const uint32_t s = __shfl_sync(0xffffffffu, slot, r + hw);
-      cp_async16(base + swz(r + hw, c), rows + s);
+      cp_async16(base + swz(r + hw, c), rows + (s + (uint32_t)c * 16u));
     }
     const uint8_t* cs = codes + (int64_t)rec * kCodeBytes;
-    for (int x = lane; x < 2 * __popc(cur); x += 32) cp_async16(code_buf + x * 16, cs + x * 16);
+    for (int x = lane; x < 2 * n_rec; x += 32) cp_async16(code_buf + x * 16, cs + x * 16);
     cp_commit();
     take(r1, t + me.step);
     r1 = load_raw(t + 2 * me.step);
@@ -339,41 +349,20 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
     __syncwarp();                                                  // the whole warp's copies have landed
     // residual rows in place: four records at a time, eight lanes each, two
     // 16-byte pieces a lane
-    int x = g;
-    for (uint32_t left = cur; left; x += 4) {
-      int tk = -1;
+    for (int x = g; x < n_rec; x += 4) {
+      const uint2 e = sm.ent[w][x];
+      const __half2 f2 = *reinterpret_cast<const __half2*>(&e.x), ca = __low2half2(f2), cb = __high2half2(f2);
+      uint8_t* row = tile + e.y + c_swz(e.y, c8);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k == g && left) tk = __ffs(left) - 1;
-        left &= left - 1;
-      }
-      const uint32_t f = __shfl_sync(0xffffffffu, fac, max(tk, 0));
-      if (tk >= 0) {
-        const __half2 f2 = *reinterpret_cast<const __half2*>(&f), ca = __low2half2(f2), cb = __high2half2(f2);
-        const __half2 tlo = __hmul2(cb, lo), thi = __hmul2(cb, hi);
-        const uint32_t t01 = *reinterpret_cast<const uint32_t*>(&tlo), t23 = *reinterpret_cast<const uint32_t*>(&thi);
-        uint8_t* row = tile + swz(tk, c8);
-        uint32_t code[2];
-        uint4 v[2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          code[y] = *reinterpret_cast<const uint16_t*>(sm.codes[w] + x * kCodeBytes + y * 16 + c8 * 2);
-          v[y] = *reinterpret_cast<const uint4*>(row + y * kHalf);
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint32_t* vw = reinterpret_cast<uint32_t*>(&v[y]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // two codes to the four byte numbers of their table entries
-            const uint32_t nn = (code[y] >> (4 * k)) & 15u;
-            const uint32_t sel = ((nn | (nn << 6)) & 0x303u) * 0x22u + 0x1010u;
-            const uint32_t lv = __byte_perm(t01, t23, sel);
-            const __half2 z = __hfma2(ca, *reinterpret_cast<const __half2*>(&vw[k]), *reinterpret_cast<const __half2*>(&lv));
-            vw[k] = *reinterpret_cast<const uint32_t*>(&z);
-          }
-          *reinterpret_cast<uint4*>(row + y * kHalf) = v[y];
-        }
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t code = *reinterpret_cast<const uint16_t*>(sm.codes[w] + x * kCodeBytes + y * 16 + c8 * 2);
+        uint4 v = *reinterpret_cast<const uint4*>(row + y * kHalf);
+        const uint2 la = sm.lut[code & 255u], lb = sm.lut[code >> 8];
+        add_levels(v.x, ca, cb, la.x);
+        add_levels(v.y, ca, cb, la.y);
+        add_levels(v.z, ca, cb, lb.x);
+        add_levels(v.w, ca, cb, lb.y);
+        *reinterpret_cast<uint4*>(row + y * kHalf) = v;
       }
     }
     tc::fence_proxy_async_smem();
@@ -469,6 +458,14 @@ __device__ __forceinline__ void tmem_wait_ld8(uint32_t (&a)[8]) {
                :
                : "memory");
 }
+// Bit x: the row of column x does not see this token.
+__device__ __noinline__ uint32_t hidden_columns(unsigned long long vis, const unsigned char* colt) {
+  uint32_t h = 0;
+#pragma unroll 1
+  for (int x = 0; x < 16; ++x) h |= (uint32_t)!((vis >> colt[x]) & 1ull) << x;
+  return h;
+}
+
 // New references of rows c1 .. c1 + 15 for a softmax group whose last tile was
 // `before` (negative: none): the maxima over the tile's tokens, the factor of the sums so far (fl), and the
 // outputs so far in tensor memory.  Out of line and in loops: it runs once or
@@ -545,7 +542,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   constexpr int CG = Shape<NC>::CG, PG = Shape<NC>::PG, kMma = Shape<NC>::kMma, kThreads = Shape<NC>::kThreads;
   extern __shared__ __align__(1024) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int part = blockIdx.x, blk = blockIdx.y, bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
   const int64_t unit = (int64_t)bh * a.n_blk + blk;
   float* ml = a.ml + (unit * a.parts + part) * NC * 2;
@@ -607,6 +604,10 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   }
   if (NC < kOCols)                                    // columns of P that no row fills
     for (int i = tid; i < 2 * kTT * 8; i += kThreads) reinterpret_cast<uint4*>(sm.P)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < 256) {
+    const auto lev = [&](int k) { const int c = (tid >> (2 * k)) & 3; return c == 0 ? a.lev[0] : c == 1 ? a.lev[1] : c == 2 ? a.lev[2] : a.lev[3]; };
+    sm.lut[tid] = make_uint2(pack_half2(lev(0), lev(1)), pack_half2(lev(2), lev(3)));
+  }
   const bool rotate = !tail && !a.naive;
   for (int c = warp; c < NC; c += kThreads / 32) {
     const int r = blk * NC + c;
@@ -715,6 +716,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         live = t < a.N;
       }
       if (!live) vis = 0;
+      const uint32_t hidden = special ? hidden_columns(vis, &sm.colt[c0]) : 0u;
       wait_b(sm, &sm.sk[i % kKSl], (i / kKSl) & 1, a);
       wait_b(sm, &sm.sv[bf], (i >> 1) & 1, a);
       const float rk = sm.rk[i % kKSl][tok], w = sm.wv[bf][tok];
@@ -727,28 +729,39 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         float pmax = 0.f, vmax = 0.f;
         uint32_t s[16];
         load_cols(scol, s);
+        float2 u[8];
 #pragma unroll
-        for (int y = 0; y < 16; y += 4) {
-          const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c0 + y]);
-          const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[par][c0 + y]);
-          const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[par][c0 + y]);
+        for (int y = 0; y < 4; ++y) {
+          const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c0 + 4 * y]);
+          const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[par][c0 + 4 * y]);
 #pragma unroll
-          for (int z = 0; z < 4; z += 2) {
-            const float2 k2 = __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk));
-            float2 u = __ffma2_rn(make_float2(__uint_as_float(s[y + z]), __uint_as_float(s[y + z + 1])), k2,
-                                  z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
-            if (special) {
-              if (!((vis >> sm.colt[c0 + y + z]) & 1ull)) u.x = -INFINITY;
-              if (!((vis >> sm.colt[c0 + y + z + 1]) & 1ull)) u.y = -INFINITY;
-            }
-            const float2 e = make_float2(tc::ex2_approx(u.x), tc::ex2_approx(u.y));
+          for (int z = 0; z < 2; ++z)
+            u[2 * y + z] = __ffma2_rn(
+                make_float2(__uint_as_float(s[4 * y + 2 * z]), __uint_as_float(s[4 * y + 2 * z + 1])),
+                __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk)),
+                z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
+        }
+        if (hidden) {
+          asm volatile("");                    // a branch: ordinary tiles should not carry this as predicated instructions
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            if ((hidden >> (2 * x)) & 1u) u[x].x = -INFINITY;
+            if ((hidden >> (2 * x + 1)) & 1u) u[x].y = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[par][c0 + 4 * y]);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float2 e = make_float2(tc::ex2_approx(u[2 * y + z].x), tc::ex2_approx(u[2 * y + z].y));
             // in this order a masked 0 stays 0 whatever the value's scale
             const float2 v = __fmul2_rn(__fmul2_rn(e, make_float2(w, w)),
                                         z ? make_float2(cw.z, cw.w) : make_float2(cw.x, cw.y));
             pmax = fmaxf(pmax, fmaxf(e.x, e.y));
             vmax = fmaxf(vmax, fmaxf(fabsf(v.x), fabsf(v.y)));
-            p[(y + z) / 2] = e;
-            pk[(y + z) / 2] = pack_half2(v.x, v.y);
+            p[2 * y + z] = e;
+            pk[2 * y + z] = pack_half2(v.x, v.y);
           }
         }
         // a second time only where infinities leave no reference
