@@ -17,8 +17,9 @@ struct TreePlan {
   int tail_parts;                    // of those, CTAs of exact tokens only (tensor-core kernel)
   int64_t cap;                       // exact tokens that the page tables can hold
   // workspace (bytes): status words, (max, sum) and outputs of every
-  // part; tensor-core kernel: rotated anchors, their scales, infinite values
-  int64_t o_ml, o_part, o_anc, o_anc_scale, o_inf, ws_total;
+  // part; tensor-core kernel: rotated anchors, their scales, token tables,
+  // infinite values
+  int64_t o_ml, o_part, o_anc, o_anc_scale, o_meta, o_inf, ws_total;
 };
 
 struct TreeArgs {
@@ -52,6 +53,7 @@ struct TreeArgs {
   float* part;                       // [unit][part][RB][D]
   void* anc;                         // [batch][2][H][k][D] fp16, rotated
   float* anc_scale;                  // [batch][2][H][k]
+  void* meta;                        // [batch][2][H][n_tiles] token tables
   unsigned long long* inf_v;         // [batch][H] drafts with an infinite or NaN value
 };
 
@@ -75,6 +77,8 @@ __device__ __forceinline__ unsigned long long tree_mask(const TreeArgs& a, int b
   return a.mask ? a.mask[(int64_t)b * a.T + t] : (2ull << t) - 1;
 }
 
+// Bytes of one tile's token table (one side and head).
+int64_t tree_meta_bytes();
 void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp);
 int launch_tree_tc(const TreeArgs& a, cudaStream_t s);
 void tree_plan_simt(const Plan& pl, TreePlan* tp);

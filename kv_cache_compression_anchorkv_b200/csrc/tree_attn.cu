@@ -36,6 +36,7 @@ int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pa
     const int64_t rows = (int64_t)tp->batch * 2 * pl->H * pl->k;
     tp->o_anc = take(2 * kD * rows);
     tp->o_anc_scale = take(4 * rows);
+    if (prefix) tp->o_meta = take(tree_meta_bytes() * tp->batch * 2 * pl->H * pl->n_tiles);
     tp->o_inf = take(8 * (int64_t)tp->batch * pl->H);
   }
   tp->ws_total = off;
@@ -126,10 +127,11 @@ int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* w
   cudaStream_t s = (cudaStream_t)stream;
   a.anc = w + tp.o_anc;
   a.anc_scale = (float*)(w + tp.o_anc_scale);
+  a.meta = w + tp.o_meta;
   a.inf_v = (unsigned long long*)(w + tp.o_inf);
   stage_begin(kStTree, s);
   st = p->dtype == ANCHORKV_BF16 ? launch_tree_tc(a, s) : launch_tree_simt(a, s);
-  stage_end(kStTree, s, p->dtype == ANCHORKV_BF16 ? 3 : 2);
+  stage_end(kStTree, s, p->dtype != ANCHORKV_BF16 ? 2 : t->compressed ? 4 : 3);
   return st;
 }
 

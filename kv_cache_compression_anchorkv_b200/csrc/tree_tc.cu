@@ -55,9 +55,10 @@ namespace akv {
 namespace {
 
 constexpr int kTT = 128;                  // tokens of a tile
-constexpr int kMaxProd = 16;              // producer warps
-constexpr int kKSt = 2, kVSt = 2;         // stages of the key and value rings
-constexpr int kKSl = kKSt + 2;            // key scales outlive their tile by the two logit buffers
+constexpr int kSt = 2;                    // stages of the key and value rings
+// Token tables are loaded four tiles ahead, when the tile four before has been
+// multiplied; a key tile's scales are read up to two tiles after that.
+constexpr int kMetaSl = 4, kKSl = 8, kVSl = 4;
 constexpr int kTileBytes = kTT * kD * 2;
 constexpr int kHalf = kTileBytes / 2;     // 64 coordinates of every row
 constexpr int kOCols = 64;                // output columns in tensor memory, twice (even and odd tiles)
@@ -72,17 +73,32 @@ constexpr float kPTarget = 5.f;
 constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
 constexpr float kRefGap = 120.f;          // the references' largest distance downwards
 
+// What a tile of one side needs beside rows and codes, written by the
+// pre-kernel: per token its scale and its anchor's byte offset, per residual
+// record its two factors and its row's byte offset in half a tile; `quarter`:
+// byte q counts the records before quarter q.
+struct Table {
+  uint32_t row[kTT];
+  uint2 ent[kTT];
+  uint32_t quarter, n_rec, first, pad;
+};
+struct Meta {
+  float scale[kTT];
+  Table table;
+};
+static_assert(sizeof(Table) % 16 == 0 && offsetof(Meta, table) % 16 == 0, "copied in 16-byte pieces");
+
 struct Sm {
-  uint8_t K[kKSt][kTileBytes];
-  uint8_t V[kVSt][kTileBytes];
+  uint8_t K[kSt][kTileBytes];
+  uint8_t V[kSt][kTileBytes];
   uint8_t P[2][kTT * 128];                // [token][64 rows] fp16, swizzled
   uint8_t Q[64 * kD * 2];
-  alignas(16) uint8_t codes[kMaxProd][32 * kCodeBytes];   // of a producer's 32 rows
-  uint2 ent[kMaxProd][32];                // their residual records: factors, row
+  alignas(16) uint8_t codes[2][kSt][kTT * kCodeBytes];    // [side][stage]
+  alignas(16) Table meta[2][kMetaSl];     // [side]
+  alignas(16) float rk[kKSl][kTT];        // key scales
+  alignas(16) float wv[kVSl][kTT];        // value scales
   uint2 lut[256];                         // code byte -> its four levels in fp16
   uint64_t drain;                         // products after a failure
-  float rk[kKSl][kTT];                    // key scales
-  float wv[kVSt][kTT];                    // value scales
   alignas(16) float cs[64];               // per row: logit scale
   // per row, of the even and the odd tiles: -reference of the sum,
   // 2^(reference of the sum - that of w p), reference of w p
@@ -92,17 +108,24 @@ struct Sm {
   float lsum[2][4][64];
   unsigned long long mask[kTreeMaxDrafts];
   unsigned char colt[64];                 // draft of each row
-  uint64_t full[2][2], kempty[kKSt], pv[2], sfull[2], sempty[2], pfull[2], sk[kKSl], sv[kVSt];   // full: [side][stage]
+  uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[kKSl], sv[kVSl];   // full: [side][stage]
+  uint64_t loaded[2][kMetaSl], coded[2][kSt];     // token tables, codes
   uint32_t tmem;
   int err, bad, rep;
 };
 static_assert(offsetof(Sm, cs) % 16 == 0 && offsetof(Sm, nm) % 16 == 0 && offsetof(Sm, cw) % 16 == 0 &&
-              offsetof(Sm, codes) % 16 == 0 && offsetof(Sm, V) % 1024 == 0 && offsetof(Sm, P) % 1024 == 0 &&
+              offsetof(Sm, codes) % 16 == 0 && offsetof(Sm, meta) % 16 == 0 && offsetof(Sm, V) % 1024 == 0 && offsetof(Sm, P) % 1024 == 0 &&
               offsetof(Sm, Q) % 1024 == 0, "16-byte reads, swizzle atoms");
-static_assert(kVSt == 2, "the value ring and the P buffers share the barrier pv");
+static_assert(kSt == 2, "the value ring and the P buffers share the barrier pv");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// `bytes` (a multiple of 16) between 16-byte aligned addresses.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
@@ -221,6 +244,53 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   }
 }
 
+// Token tables of every layout in use, one warp per 32 tokens of a side and
+// head, after the anchors' scales: what a token row is multiplied by,
+// w_t = gamma_t M_a or sigma_t where that is larger, and a residual row's
+// factors (one of the two is 1).  Bound by latency and the tables' writes
+// (2 KB a tile and side).
+__global__ void __launch_bounds__(256) tree_meta_kernel(TreeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, b = blockIdx.z, sh = blockIdx.y;
+  const int tile = blockIdx.x * 2 + (threadIdx.x >> 7), t = tile * kTT + q * 32 + lane;
+  if (tile >= a.n_tiles || first_with_layout(a, b) != b) return;
+  const int lay = tree_layout(a, b);
+  if (lay < 0) return;
+  const uint8_t* comp = a.comp + (int64_t)lay * a.stride;
+  const uint32_t word = t < a.N ? reinterpret_cast<const uint32_t*>(comp + a.off_tok)[(int64_t)sh * a.N + t] : 0u;
+  const uint4 bm = *reinterpret_cast<const uint4*>(comp + a.off_bm + ((int64_t)sh * a.n_tiles + tile) * 16);
+  const int first = reinterpret_cast<const int*>(comp + a.off_pf)[(int64_t)sh * (a.n_tiles + 1) + tile];
+  // bits behind the last token mean nothing, records outside the layout are none
+  uint32_t bits[4] = {bm.x, bm.y, bm.z, bm.w};
+  int before[5] = {0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int left = a.N - (tile * kTT + k * 32);
+    if (left < 32) bits[k] &= left > 0 ? (1u << left) - 1u : 0u;
+    before[k + 1] = before[k] + __popc(bits[k]);
+  }
+  const bool fine = first >= 0 && first + (int64_t)before[4] <= a.R;
+  const uint32_t mine = q == 0 ? bits[0] : q == 1 ? bits[1] : q == 2 ? bits[2] : bits[3];
+  const int x = (q == 0 ? 0 : q == 1 ? before[1] : q == 2 ? before[2] : before[3]) + __popc(mine & ((1u << lane) - 1u));
+  const bool res = fine && ((mine >> lane) & 1u);
+  const int slot = min((int)(word & 0xffffu), a.k - 1);
+  const int64_t row0 = ((int64_t)b * 2 * a.H + sh) * a.k;
+  const float sg = res ? half_bits_to_f(reinterpret_cast<const uint16_t*>(comp + a.off_sig)[first + x]) : 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float c1 = half_bits_to_f(word >> 16) * a.anc_scale[row0 + slot];
+  const float sc = fabsf(c1) >= sg ? c1 : sg, inv = sc != 0.f ? 1.f / sc : 0.f;
+  Meta* m = reinterpret_cast<Meta*>(a.meta) + ((int64_t)b * 2 * a.H + sh) * a.n_tiles + tile;
+  m->scale[q * 32 + lane] = sc;                          // 0 behind the last token, whose word is 0
+  m->table.row[q * 32 + lane] = (uint32_t)slot * (kD * 2);
+  if (res) m->table.ent[x] = make_uint2(pack_half2(c1 * inv, sg * inv), (uint32_t)(q * 32 + lane) * 128u);
+  if (q == 0 && lane == 0) {
+    m->table.quarter = fine ? (uint32_t)before[1] << 8 | (uint32_t)before[2] << 16 | (uint32_t)before[3] << 24 : 0u;
+    m->table.n_rec = fine ? (uint32_t)before[4] : 0u;
+    m->table.first = fine ? (uint32_t)first : 0u;
+    m->table.pad = 0u;
+  }
+}
+
 // Waits for a phase.  A phase that is over already, the usual case in a full
 // pipeline, costs one test; the bounded wait is out of the way of that path.
 __device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, int* err, int* counters) {
@@ -251,111 +321,83 @@ __device__ __forceinline__ void wait_free(Sm& sm, int side, int t, const TreeArg
   if (t >= 2) wait_b(sm, side ? &sm.pv[t & 1] : &sm.kempty[t & 1], ((t >> 1) - 1) & 1, a);
 }
 
-__device__ __forceinline__ float* scales_of(Sm& sm, int side, int t) { return side ? sm.wv[t % kVSt] : sm.rk[t % kKSl]; }
-__device__ __forceinline__ void scales_done(Sm& sm, int side, int t) {
-  tc::mbar_arrive(side ? &sm.sv[t % kVSt] : &sm.sk[t % kKSl]);
-}
-
-// What a quarter's 32 tokens are, one per lane, as loaded: token word, the
-// tile's bitmap and its first record.
-struct Raw {
-  uint32_t word;
-  uint4 bm;
-  int rec;
-};
+__device__ __forceinline__ float* scales_of(Sm& sm, int side, int t) { return side ? sm.wv[t % kVSl] : sm.rk[t % kKSl]; }
+__device__ __forceinline__ uint64_t* scales_bar(Sm& sm, int side, int t) { return side ? &sm.sv[t % kVSl] : &sm.sk[t % kKSl]; }
 
 // x = ca x + cb level, two coordinates.
 __device__ __forceinline__ void add_levels(uint32_t& x, __half2 ca, __half2 cb, uint32_t level) {
   const __half2 r = __hfma2(cb, *reinterpret_cast<const __half2*>(&level), __hmul2(ca, *reinterpret_cast<const __half2*>(&x)));
   x = *reinterpret_cast<const uint32_t*>(&r);
 }
-// Where piece c (of the first half) of the row at byte offset `row` lies in it.
-__device__ __forceinline__ uint32_t c_swz(uint32_t row, int c) { return (uint32_t)(c ^ (int)((row >> 7) & 7u)) << 4; }
+
+// Token tables and codes of one side, by one lane: tables four tiles ahead,
+// codes two.  Both are due when the tile four before has been multiplied.
+__device__ void load_side(const TreeArgs& a, Sm& sm, int side, int n, const uint8_t* comp, const Meta* meta) {
+  const uint8_t* codes = comp + a.off_codes;
+  for (int t = 0; t < n + 2; ++t) {
+    if (t >= 4) wait_b(sm, side ? &sm.pv[t & 1] : &sm.kempty[t & 1], ((t - 4) >> 1) & 1, a);
+    if (t < n) {
+      uint64_t* sb = scales_bar(sm, side, t);
+      tc::mbar_expect_tx(sb, kTT * 4);
+      bulk_copy(tc::smem_u32(scales_of(sm, side, t)), meta[t].scale, kTT * 4, tc::smem_u32(sb));
+      uint64_t* mb = &sm.loaded[side][t % kMetaSl];
+      tc::mbar_expect_tx(mb, sizeof(Table));
+      bulk_copy(tc::smem_u32(&sm.meta[side][t % kMetaSl]), &meta[t].table, sizeof(Table), tc::smem_u32(mb));
+    }
+    const int c = t - 2;                                           // this tile's codes: its stage is free
+    if (c >= 0) {
+      wait_b(sm, &sm.loaded[side][c % kMetaSl], (c / kMetaSl) & 1, a);
+      const Table* m = &sm.meta[side][c % kMetaSl];
+      const uint32_t bytes = min(m->n_rec, (uint32_t)kTT) * kCodeBytes;
+      uint64_t* cb = &sm.coded[side][c & 1];
+      tc::mbar_expect_tx(cb, bytes);
+      if (bytes) bulk_copy(tc::smem_u32(sm.codes[side][c & 1]), codes + (int64_t)m->first * kCodeBytes, bytes, tc::smem_u32(cb));
+    }
+  }
+  // the copies are over before this CTA's shared memory is, also after a failure
+  for (int t = max(0, n - 4); t < n; ++t) {
+    tc::mbar_wait(&sm.loaded[side][t % kMetaSl], (t / kMetaSl) & 1);
+    tc::mbar_wait(scales_bar(sm, side, t), (t / (side ? kVSl : kKSl)) & 1);
+  }
+  for (int t = max(0, n - 2); t < n; ++t) tc::mbar_wait(&sm.coded[side][t & 1], (t >> 1) & 1);
+}
 
 template <int kProd>
-__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* comp, int rep, int h, int tile0) {
+__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* rows) {
   const Lane me = lane_of<kProd>(w);
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4, c8 = lane & 7, g = lane >> 3;
-  const int sh = me.side * a.H + h;
-  const int64_t row0 = ((int64_t)rep * 2 * a.H + sh) * a.k;
-  const uint8_t* rows = reinterpret_cast<const uint8_t*>(a.anc) + row0 * (kD * 2);
-  const float* scale = a.anc_scale + row0;
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(comp + a.off_tok) + (int64_t)sh * a.N;
-  const uint4* bms = reinterpret_cast<const uint4*>(comp + a.off_bm) + (int64_t)sh * a.n_tiles;
-  const int* pfs = reinterpret_cast<const int*>(comp + a.off_pf) + (int64_t)sh * (a.n_tiles + 1);
-  const uint8_t* codes = comp + a.off_codes;
-  const uint16_t* sig = reinterpret_cast<const uint16_t*>(comp + a.off_sig);
-  const uint32_t below = (1u << lane) - 1u, code_buf = tc::smem_u32(sm.codes[w]);
-
-  auto load_raw = [&](int t) {
-    Raw r = {0u, make_uint4(0u, 0u, 0u, 0u), 0};
-    if (t < n) {
-      const int tile = tile0 + t, at = tile * kTT + me.q * 32 + lane;
-      if (at < a.N) r.word = words[at];
-      r.bm = bms[tile];
-      r.rec = pfs[tile];
-    }
-    return r;
-  };
-  // this quarter's words of a tile: residual bits and the first one's record
-  uint32_t word = 0, bits = 0;
-  int rec = 0;
-  float m = 0.f, sg = 0.f;
-  auto take = [&](const Raw& r, int t) {
-    word = r.word;
-    bits = me.q == 0 ? r.bm.x : me.q == 1 ? r.bm.y : me.q == 2 ? r.bm.z : r.bm.w;
-    rec = r.rec;
-    if (me.q > 0) rec += __popc(r.bm.x);
-    if (me.q > 1) rec += __popc(r.bm.y);
-    if (me.q > 2) rec += __popc(r.bm.z);
-    const int left = a.N - ((tile0 + t) * kTT + me.q * 32);        // bits behind the last token mean nothing
-    if (left < 32) bits &= left > 0 ? (1u << left) - 1u : 0u;
-    if (rec < 0 || rec + (int64_t)__popc(bits) > a.R) bits = 0u;
-    m = scale[min((int)(word & 0xffffu), a.k - 1)];
-    sg = (bits >> lane) & 1u ? half_bits_to_f(sig[rec + __popc(bits & below)]) : 0.f;
-  };
-
-  // token words two tiles ahead, what hangs on them one tile ahead
-  Raw r0 = load_raw(me.first);
-  Raw r1 = load_raw(me.first + me.step);
-  take(r0, me.first);
+  rows += c * 16;
   for (int t = me.first; t < n; t += me.step) {
-    // scale of the row; a residual's row keeps the larger of its two factors at 1
-    const float c1 = half_bits_to_f(word >> 16) * m;
-    const float sc = fabsf(c1) >= sg ? c1 : sg;
-    const float inv = sc != 0.f ? __fdividef(1.f, sc) : 0.f;
-    const int n_rec = __popc(bits);
-    wait_free(sm, me.side, t, a);
-    scales_of(sm, me.side, t)[me.q * 32 + lane] = sc;             // 0 behind the last token, whose word is 0
-    __syncwarp();
-    if (lane == 0) scales_done(sm, me.side, t);
-    if ((bits >> lane) & 1u)
-      sm.ent[w][__popc(bits & below)] = make_uint2(pack_half2(c1 * inv, sg * inv), (uint32_t)lane * 128u);
-    // anchor rows, sixteen lanes each; the residuals' codes as one block
-    uint8_t* tile = (me.side ? sm.V[t & 1] : sm.K[t & 1]) + me.q * 32 * 128;
-    const uint32_t base = tc::smem_u32(tile);
-    const uint32_t slot = (uint32_t)min((int)(word & 0xffffu), a.k - 1) * (kD * 2);
+    wait_b(sm, &sm.loaded[me.side][t % kMetaSl], (t / kMetaSl) & 1, a);
+    const Table* m = &sm.meta[me.side][t % kMetaSl];
+    // anchor rows, sixteen lanes each: the first half of the quarter by the
+    // first half of the warp
+    uint4 off[4];
 #pragma unroll
-    for (int r = 0; r < 32; r += 2) {
-      const uint32_t s = __shfl_sync(0xffffffffu, slot, r + hw);
-      cp_async16(base + swz(r + hw, c), rows + (s + (uint32_t)c * 16u));
+    for (int k = 0; k < 4; ++k) off[k] = *reinterpret_cast<const uint4*>(&m->row[me.q * 32 + hw * 16 + k * 4]);
+    wait_free(sm, me.side, t, a);
+    uint8_t* tile = me.side ? sm.V[t & 1] : sm.K[t & 1];
+    const uint32_t base = tc::smem_u32(tile) + (c >> 3) * kHalf + (me.q * 32 + hw * 16) * 128;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint32_t o = k % 4 == 0 ? off[k / 4].x : k % 4 == 1 ? off[k / 4].y : k % 4 == 2 ? off[k / 4].z : off[k / 4].w;
+      cp_async16(base + k * 128 + ((c8 ^ (k & 7)) << 4), rows + o);
     }
-    const uint8_t* cs = codes + (int64_t)rec * kCodeBytes;
-    for (int x = lane; x < 2 * n_rec; x += 32) cp_async16(code_buf + x * 16, cs + x * 16);
     cp_commit();
-    take(r1, t + me.step);
-    r1 = load_raw(t + 2 * me.step);
+    const int x0 = (m->quarter >> (8 * me.q)) & 255, x1 = me.q < 3 ? (m->quarter >> (8 * me.q + 8)) & 255 : m->n_rec;
+    wait_b(sm, &sm.coded[me.side][t & 1], (t >> 1) & 1, a);
+    const uint8_t* cd = sm.codes[me.side][t & 1] + c8 * 2;
     cp_wait();
     __syncwarp();                                                  // the whole warp's copies have landed
     // residual rows in place: four records at a time, eight lanes each, two
     // 16-byte pieces a lane
-    for (int x = g; x < n_rec; x += 4) {
-      const uint2 e = sm.ent[w][x];
+    for (int x = x0 + g; x < x1; x += 4) {
+      const uint2 e = m->ent[x];
       const __half2 f2 = *reinterpret_cast<const __half2*>(&e.x), ca = __low2half2(f2), cb = __high2half2(f2);
-      uint8_t* row = tile + e.y + c_swz(e.y, c8);
+      uint8_t* row = tile + e.y + ((c8 ^ ((e.y >> 7) & 7u)) << 4);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const uint32_t code = *reinterpret_cast<const uint16_t*>(sm.codes[w] + x * kCodeBytes + y * 16 + c8 * 2);
+        const uint32_t code = *reinterpret_cast<const uint16_t*>(cd + x * kCodeBytes + y * 16);
         uint4 v = *reinterpret_cast<const uint4*>(row + y * kHalf);
         const uint2 la = sm.lut[code & 255u], lb = sm.lut[code >> 8];
         add_levels(v.x, ca, cb, la.x);
@@ -434,7 +476,7 @@ __device__ void produce_tail(const TreeArgs& a, Sm& sm, int w, int n, int b, int
     tc::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      scales_done(sm, me.side, tl);
+      tc::mbar_arrive(scales_bar(sm, me.side, tl));
       tc::mbar_arrive(&sm.full[me.side][tl & 1]);
     }
   }
@@ -530,11 +572,12 @@ __device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t 
 
 // NC: rows (columns of the accumulators) of a CTA.  Softmax groups of four
 // warps have 16 of the rows each, and every tile or (PG = 2) every other tile;
-// then the warp that issues the MMAs, then the producers.
+// then the warp that issues the MMAs, a loader of token tables for each side,
+// then the producers.
 template <int NC>
 struct Shape {
   static constexpr int CG = NC / 16, PG = NC == 16 ? 2 : 1, kProd = NC == 64 ? 8 : 16;
-  static constexpr int kMma = 4 * CG * PG, kFirstProd = kMma + 1, kThreads = 32 * (kFirstProd + kProd);
+  static constexpr int kMma = 4 * CG * PG, kLoad = kMma + 1, kFirstProd = kMma + 3, kThreads = 32 * (kFirstProd + kProd);
 };
 
 template <int NC>
@@ -575,8 +618,13 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kKSl; ++i) tc::mbar_init(&sm.sk[i], 4);          // four quarters of a tile
-    for (int i = 0; i < kVSt; ++i) tc::mbar_init(&sm.sv[i], 4);
+    // scales: one copy a tile, or four quarters of exact rows
+    for (int i = 0; i < kKSl; ++i) tc::mbar_init(&sm.sk[i], tail ? 4 : 1);
+    for (int i = 0; i < kVSl; ++i) tc::mbar_init(&sm.sv[i], tail ? 4 : 1);
+    for (int s = 0; s < 2; ++s) {
+      for (int i = 0; i < kMetaSl; ++i) tc::mbar_init(&sm.loaded[s][i], 1);
+      for (int i = 0; i < kSt; ++i) tc::mbar_init(&sm.coded[s][i], 1);
+    }
     tc::mbar_init(&sm.drain, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.full[0][i], 4);
@@ -644,7 +692,15 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     // ---- rows of the key and value tiles
     const int w = warp - Shape<NC>::kFirstProd;
     if (tail) produce_tail<Shape<NC>::kProd>(a, sm, w, n, b, h, tile0, len, n_new);
-    else produce_prefix<Shape<NC>::kProd>(a, sm, w, n, a.comp + (int64_t)lay * a.stride, sm.rep, h, tile0);
+    else produce_prefix<Shape<NC>::kProd>(a, sm, w, n, reinterpret_cast<const uint8_t*>(a.anc) +
+                                                           (((int64_t)sm.rep * 2 + ((w >> 2) & 1)) * a.H + h) * a.k * (kD * 2));
+  } else if (warp > kMma) {
+    if (!tail && lane == 0) {
+      const int side = warp - Shape<NC>::kLoad;
+      load_side(a, sm, side, n, a.comp + (int64_t)lay * a.stride,
+                reinterpret_cast<const Meta*>(a.meta) + (((int64_t)sm.rep * 2 + side) * a.H + h) * a.n_tiles + tile0);
+    }
+    __syncwarp();
   } else if (warp == kMma) {
     {
       // ---- MMA issue
@@ -718,8 +774,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       if (!live) vis = 0;
       const uint32_t hidden = special ? hidden_columns(vis, &sm.colt[c0]) : 0u;
       wait_b(sm, &sm.sk[i % kKSl], (i / kKSl) & 1, a);
-      wait_b(sm, &sm.sv[bf], (i >> 1) & 1, a);
-      const float rk = sm.rk[i % kKSl][tok], w = sm.wv[bf][tok];
+      wait_b(sm, &sm.sv[i % kVSl], (i / kVSl) & 1, a);
+      const float rk = sm.rk[i % kKSl][tok], w = sm.wv[i % kVSl][tok];
       wait_b(sm, &sm.sfull[bf], (i >> 1) & 1, a);
       tc::fence_after_sync();
       const uint32_t scol = tmem + lane_base + kSCol + bf * NC + c0;
@@ -952,13 +1008,18 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   const int gx = a.comp ? std::max(1, std::min((a.k + 7) / 8, 256)) : 1;
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  int st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, s, a);
+  int st = ANCHORKV_OK;
+  if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 1) / 2, 2 * a.H, a.batch), 256, 0, s, a);
+  if (st) return st;
+  st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, s, a);
   if (st) return st;
   const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
   return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 7) / 8)), 256, 0, s, a);
 }
 
 }  // namespace
+
+int64_t tree_meta_bytes() { return (int64_t)sizeof(Meta); }
 
 void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
   tp->RB = tp->rows <= 16 ? 16 : tp->rows <= 32 ? 32 : 64;
