@@ -59,6 +59,7 @@ constexpr int kSt = 2;                    // stages of the key and value rings
 // Token tables are loaded four tiles ahead, when the tile four before has been
 // multiplied; a key tile's scales are read up to two tiles after that.
 constexpr int kMetaSl = 4, kKSl = 8, kVSl = 4;
+constexpr int kCodeSl = 3;                // codes, three tiles ahead: they come from HBM
 constexpr int kTileBytes = kTT * kD * 2;
 constexpr int kHalf = kTileBytes / 2;     // 64 coordinates of every row
 constexpr int kOCols = 64;                // output columns in tensor memory, twice (even and odd tiles)
@@ -74,12 +75,13 @@ constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
 constexpr float kRefGap = 120.f;          // the references' largest distance downwards
 
 // What a tile of one side needs beside rows and codes, written by the
-// pre-kernel: per token its scale and its anchor's byte offset, per residual
-// record its two factors and its row's byte offset in half a tile; `quarter`:
-// byte q counts the records before quarter q.
+// pre-kernel: per token its scale and its anchor slot; per residual record the
+// factors of its anchor and its levels (fp16, one of them 1) and its token;
+// `quarter`: byte q counts the records before quarter q.
 struct Table {
-  uint32_t row[kTT];
-  uint2 ent[kTT];
+  uint16_t slot[kTT];
+  uint32_t fac[kTT];
+  uint8_t tok[kTT];
   uint32_t quarter, n_rec, first, pad;
 };
 struct Meta {
@@ -93,23 +95,23 @@ struct Sm {
   uint8_t V[kSt][kTileBytes];
   uint8_t P[2][kTT * 128];                // [token][64 rows] fp16, swizzled
   uint8_t Q[64 * kD * 2];
-  alignas(16) uint8_t codes[2][kSt][kTT * kCodeBytes];    // [side][stage]
+  alignas(16) uint8_t codes[2][kCodeSl][kTT * kCodeBytes];        // [side]
   alignas(16) Table meta[2][kMetaSl];     // [side]
   alignas(16) float rk[kKSl][kTT];        // key scales
   alignas(16) float wv[kVSl][kTT];        // value scales
-  uint2 lut[256];                         // code byte -> its four levels in fp16
+  uint32_t lut[16];                       // two codes -> their levels in fp16
   uint64_t drain;                         // products after a failure
   alignas(16) float cs[64];               // per row: logit scale
   // per row, of the even and the odd tiles: -reference of the sum,
   // 2^(reference of the sum - that of w p), reference of w p
   alignas(16) float nm[2][64], cw[2][64], mp[2][64];
-  float fl[2][64];                        // rescaling of the sums
+  float fl[2][64];                        // rescaling of the sums; at the end of the outputs
   int red[2][2][4][64];
   float lsum[2][4][64];
   unsigned long long mask[kTreeMaxDrafts];
   unsigned char colt[64];                 // draft of each row
   uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[kKSl], sv[kVSl];   // full: [side][stage]
-  uint64_t loaded[2][kMetaSl], coded[2][kSt];     // token tables, codes
+  uint64_t loaded[2][kMetaSl], coded[2][kCodeSl];     // token tables, codes
   uint32_t tmem;
   int err, bad, rep;
 };
@@ -139,6 +141,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // where its inverse is a normal number too.
 __device__ __forceinline__ int scale_exp(uint32_t bits) { return min(max((int)(bits >> 23), 1), 253); }
 __device__ __forceinline__ float exp_to_f(int e) { return __uint_as_float((uint32_t)e << 23); }       // 2^(e - 127)
+// 2^d of a whole number d, 0 below fp32's normal range.
+__device__ __forceinline__ float pow2(float d) {
+  return d < -126.f ? 0.f : __int_as_float(((int)fminf(d, 128.f) + 127) << 23);
+}
 __device__ __forceinline__ float exp_to_inv(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
 __device__ __forceinline__ uint32_t bar_or(int id, int count, bool p) {
@@ -281,8 +287,11 @@ __global__ void __launch_bounds__(256) tree_meta_kernel(TreeArgs a) {
   const float sc = fabsf(c1) >= sg ? c1 : sg, inv = sc != 0.f ? 1.f / sc : 0.f;
   Meta* m = reinterpret_cast<Meta*>(a.meta) + ((int64_t)b * 2 * a.H + sh) * a.n_tiles + tile;
   m->scale[q * 32 + lane] = sc;                          // 0 behind the last token, whose word is 0
-  m->table.row[q * 32 + lane] = (uint32_t)slot * (kD * 2);
-  if (res) m->table.ent[x] = make_uint2(pack_half2(c1 * inv, sg * inv), (uint32_t)(q * 32 + lane) * 128u);
+  m->table.slot[q * 32 + lane] = (uint16_t)slot;
+  if (res) {
+    m->table.fac[x] = pack_half2(c1 * inv, sg * inv);
+    m->table.tok[x] = (uint8_t)(q * 32 + lane);
+  }
   if (q == 0 && lane == 0) {
     m->table.quarter = fine ? (uint32_t)before[1] << 8 | (uint32_t)before[2] << 16 | (uint32_t)before[3] << 24 : 0u;
     m->table.n_rec = fine ? (uint32_t)before[4] : 0u;
@@ -331,27 +340,28 @@ __device__ __forceinline__ void add_levels(uint32_t& x, __half2 ca, __half2 cb, 
 }
 
 // Token tables and codes of one side, by one lane: tables four tiles ahead,
-// codes two.  Both are due when the tile four before has been multiplied.
+// codes three.  Both are due when the tile four before the table's, whose
+// places they take, has been multiplied.
 __device__ void load_side(const TreeArgs& a, Sm& sm, int side, int n, const uint8_t* comp, const Meta* meta) {
   const uint8_t* codes = comp + a.off_codes;
-  for (int t = 0; t < n + 2; ++t) {
+  for (int t = 0; t <= n; ++t) {
     if (t >= 4) wait_b(sm, side ? &sm.pv[t & 1] : &sm.kempty[t & 1], ((t - 4) >> 1) & 1, a);
     if (t < n) {
-      uint64_t* sb = scales_bar(sm, side, t);
-      tc::mbar_expect_tx(sb, kTT * 4);
-      bulk_copy(tc::smem_u32(scales_of(sm, side, t)), meta[t].scale, kTT * 4, tc::smem_u32(sb));
       uint64_t* mb = &sm.loaded[side][t % kMetaSl];
       tc::mbar_expect_tx(mb, sizeof(Table));
       bulk_copy(tc::smem_u32(&sm.meta[side][t % kMetaSl]), &meta[t].table, sizeof(Table), tc::smem_u32(mb));
+      uint64_t* sb = scales_bar(sm, side, t);
+      tc::mbar_expect_tx(sb, kTT * 4);
+      bulk_copy(tc::smem_u32(scales_of(sm, side, t)), meta[t].scale, kTT * 4, tc::smem_u32(sb));
     }
-    const int c = t - 2;                                           // this tile's codes: its stage is free
+    const int c = t - 1;
     if (c >= 0) {
       wait_b(sm, &sm.loaded[side][c % kMetaSl], (c / kMetaSl) & 1, a);
       const Table* m = &sm.meta[side][c % kMetaSl];
       const uint32_t bytes = min(m->n_rec, (uint32_t)kTT) * kCodeBytes;
-      uint64_t* cb = &sm.coded[side][c & 1];
+      uint64_t* cb = &sm.coded[side][c % kCodeSl];
       tc::mbar_expect_tx(cb, bytes);
-      if (bytes) bulk_copy(tc::smem_u32(sm.codes[side][c & 1]), codes + (int64_t)m->first * kCodeBytes, bytes, tc::smem_u32(cb));
+      if (bytes) bulk_copy(tc::smem_u32(sm.codes[side][c % kCodeSl]), codes + (int64_t)m->first * kCodeBytes, bytes, tc::smem_u32(cb));
     }
   }
   // the copies are over before this CTA's shared memory is, also after a failure
@@ -359,7 +369,7 @@ __device__ void load_side(const TreeArgs& a, Sm& sm, int side, int n, const uint
     tc::mbar_wait(&sm.loaded[side][t % kMetaSl], (t / kMetaSl) & 1);
     tc::mbar_wait(scales_bar(sm, side, t), (t / (side ? kVSl : kKSl)) & 1);
   }
-  for (int t = max(0, n - 2); t < n; ++t) tc::mbar_wait(&sm.coded[side][t & 1], (t >> 1) & 1);
+  for (int t = max(0, n - kCodeSl); t < n; ++t) tc::mbar_wait(&sm.coded[side][t % kCodeSl], (t / kCodeSl) & 1);
 }
 
 template <int kProd>
@@ -372,39 +382,54 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
     const Table* m = &sm.meta[me.side][t % kMetaSl];
     // anchor rows, sixteen lanes each: the first half of the quarter by the
     // first half of the warp
-    uint4 off[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) off[k] = *reinterpret_cast<const uint4*>(&m->row[me.q * 32 + hw * 16 + k * 4]);
+    const uint4 sa = *reinterpret_cast<const uint4*>(&m->slot[me.q * 32 + hw * 16]);
+    const uint4 sb = *reinterpret_cast<const uint4*>(&m->slot[me.q * 32 + hw * 16 + 8]);
+    const uint32_t slots[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
     wait_free(sm, me.side, t, a);
     uint8_t* tile = me.side ? sm.V[t & 1] : sm.K[t & 1];
     const uint32_t base = tc::smem_u32(tile) + (c >> 3) * kHalf + (me.q * 32 + hw * 16) * 128;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const uint32_t o = k % 4 == 0 ? off[k / 4].x : k % 4 == 1 ? off[k / 4].y : k % 4 == 2 ? off[k / 4].z : off[k / 4].w;
+      // 256 bytes a row: the slot's two bytes one byte up
+      const uint32_t o = __byte_perm(slots[k / 2], 0u, k & 1 ? 0x4324u : 0x4104u);
       cp_async16(base + k * 128 + ((c8 ^ (k & 7)) << 4), rows + o);
     }
     cp_commit();
     const int x0 = (m->quarter >> (8 * me.q)) & 255, x1 = me.q < 3 ? (m->quarter >> (8 * me.q + 8)) & 255 : m->n_rec;
-    wait_b(sm, &sm.coded[me.side][t & 1], (t >> 1) & 1, a);
-    const uint8_t* cd = sm.codes[me.side][t & 1] + c8 * 2;
+    wait_b(sm, &sm.coded[me.side][t % kCodeSl], (t / kCodeSl) & 1, a);
+    const uint8_t* cd = sm.codes[me.side][t % kCodeSl] + c8 * 2;
     cp_wait();
     __syncwarp();                                                  // the whole warp's copies have landed
-    // residual rows in place: four records at a time, eight lanes each, two
-    // 16-byte pieces a lane
-    for (int x = x0 + g; x < x1; x += 4) {
-      const uint2 e = m->ent[x];
-      const __half2 f2 = *reinterpret_cast<const __half2*>(&e.x), ca = __low2half2(f2), cb = __high2half2(f2);
-      uint8_t* row = tile + e.y + ((c8 ^ ((e.y >> 7) & 7u)) << 4);
+    // residual rows in place: eight records at a time, eight lanes each for two
+    // of them, two 16-byte pieces a lane; all reads before the writes
+    for (int x = x0 + g; x < x1; x += 8) {
+      const bool two = x + 4 < x1;
+      uint8_t* row[2];
+      uint32_t f[2], code[2][2];
+      uint4 v[2][2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const uint32_t code = *reinterpret_cast<const uint16_t*>(cd + x * kCodeBytes + y * 16);
-        uint4 v = *reinterpret_cast<const uint4*>(row + y * kHalf);
-        const uint2 la = sm.lut[code & 255u], lb = sm.lut[code >> 8];
-        add_levels(v.x, ca, cb, la.x);
-        add_levels(v.y, ca, cb, la.y);
-        add_levels(v.z, ca, cb, lb.x);
-        add_levels(v.w, ca, cb, lb.y);
-        *reinterpret_cast<uint4*>(row + y * kHalf) = v;
+      for (int k = 0; k < 2; ++k) {
+        const int y = k && two ? x + 4 : x;
+        const uint32_t tk = m->tok[y];
+        f[k] = m->fac[y];
+        row[k] = tile + tk * 128 + ((c8 ^ (tk & 7u)) << 4);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          code[k][p] = *reinterpret_cast<const uint16_t*>(cd + y * kCodeBytes + p * 16);
+          v[k][p] = *reinterpret_cast<const uint4*>(row[k] + p * kHalf);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (k && !two) break;
+        const __half2 f2 = *reinterpret_cast<const __half2*>(&f[k]), ca = __low2half2(f2), cb = __high2half2(f2);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t* vw = reinterpret_cast<uint32_t*>(&v[k][p]);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) add_levels(vw[z], ca, cb, sm.lut[(code[k][p] >> (4 * z)) & 15u]);
+          *reinterpret_cast<uint4*>(row[k] + p * kHalf) = v[k][p];
+        }
       }
     }
     tc::fence_proxy_async_smem();
@@ -494,6 +519,13 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
                : "r"(taddr)
                : "memory");
 }
+// ... four columns, complete on return.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld8(uint32_t (&a)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7])
@@ -514,7 +546,7 @@ __device__ __noinline__ uint32_t hidden_columns(unsigned long long vis, const un
 // twice, and its code should not push the tile loops out of the instruction
 // caches.
 __device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t scol, uint32_t ocol, int c1, int par,
-                                            int before, int bar_id, float rk, float w, unsigned long long vis) {
+                                            int before, int bar_id, float rk, float w, uint32_t hidden) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, tok = threadIdx.x & 127;
   const float lw = w != 0.f ? __log2f(fabsf(w)) : -INFINITY;
 #pragma unroll 1
@@ -525,7 +557,7 @@ __device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t 
 #pragma unroll
     for (int y = 0; y < 8; ++y) {
       const int c = c1 + x + y;
-      float lg = (vis >> sm.colt[c]) & 1ull ? __uint_as_float(s[y]) * (rk * sm.cs[c]) : -INFINITY;
+      float lg = (hidden >> (x + y)) & 1u ? -INFINITY : __uint_as_float(s[y]) * (rk * sm.cs[c]);
       lg = fmaxf(lg, -INFINITY);                                   // a NaN is no maximum
       const int m1 = __reduce_max_sync(0xffffffffu, ordered(lg));
       const int m2 = __reduce_max_sync(0xffffffffu, ordered(lg + lw));
@@ -546,12 +578,12 @@ __device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t 
     const float l_new = fmaxf(l_old, ceilf(m1));
     float p_new = fmaxf(p_old, ceilf(m2) + kPTarget);
     if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
-    sm.fl[par][c] = l_old > -INFINITY ? exp2f(l_old - l_new) : 0.f;
+    sm.fl[par][c] = l_old > -INFINITY ? pow2(l_old - l_new) : 0.f;
     sm.nm[par][c] = -l_new;
     sm.mp[par][c] = p_new;
-    sm.cw[par][c] = l_new > -INFINITY ? exp2f(l_new - p_new) : 1.f;
+    sm.cw[par][c] = l_new > -INFINITY ? pow2(l_new - p_new) : 1.f;
     __syncwarp(0xffffu);
-    factor[tok] = p_old > -INFINITY ? exp2f(p_old - p_new) : 0.f;
+    factor[tok] = p_old > -INFINITY ? pow2(p_old - p_new) : 0.f;
   }
   tc::named_bar(bar_id, 128);
   if (before >= 0) {
@@ -617,29 +649,29 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     tc::tmem_alloc(&sm.tmem, kTmemCols);
     tc::tmem_relinquish();
   }
-  if (tid == 0) {
-    // scales: one copy a tile, or four quarters of exact rows
-    for (int i = 0; i < kKSl; ++i) tc::mbar_init(&sm.sk[i], tail ? 4 : 1);
-    for (int i = 0; i < kVSl; ++i) tc::mbar_init(&sm.sv[i], tail ? 4 : 1);
-    for (int s = 0; s < 2; ++s) {
-      for (int i = 0; i < kMetaSl; ++i) tc::mbar_init(&sm.loaded[s][i], 1);
-      for (int i = 0; i < kSt; ++i) tc::mbar_init(&sm.coded[s][i], 1);
+  if (warp == 0) {
+    // scales: one copy a tile, or four quarters of exact rows; softmax: one
+    // arrival a warp
+    if (lane < kKSl) tc::mbar_init(&sm.sk[lane], tail ? 4 : 1);
+    if (lane < kVSl) tc::mbar_init(&sm.sv[lane], tail ? 4 : 1);
+    if (lane < 2 * kMetaSl) tc::mbar_init(&sm.loaded[0][0] + lane, 1);
+    if (lane < 2 * kCodeSl) tc::mbar_init(&sm.coded[0][0] + lane, 1);
+    if (lane < 4) tc::mbar_init(&sm.full[0][0] + lane, 4);
+    if (lane < 2) {
+      tc::mbar_init(&sm.kempty[lane], 1);
+      tc::mbar_init(&sm.pv[lane], 1);
+      tc::mbar_init(&sm.sfull[lane], 1);
+      tc::mbar_init(&sm.sempty[lane], 4 * CG);
+      tc::mbar_init(&sm.pfull[lane], 4 * CG);
     }
-    tc::mbar_init(&sm.drain, 1);
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.full[0][i], 4);
-      tc::mbar_init(&sm.full[1][i], 4);
-      tc::mbar_init(&sm.kempty[i], 1);
-      tc::mbar_init(&sm.pv[i], 1);
-      tc::mbar_init(&sm.sfull[i], 1);
-      tc::mbar_init(&sm.sempty[i], 4 * CG);                              // one arrival a warp
-      tc::mbar_init(&sm.pfull[i], 4 * CG);
+    if (lane == 0) {
+      tc::mbar_init(&sm.drain, 1);
+      sm.err = 0;
+      sm.bad = 0;
     }
     tc::fence_barrier_init();
-    sm.err = 0;
-    sm.bad = 0;
-    sm.rep = first_with_layout(a, b);
   }
+  if (tid == 32) sm.rep = first_with_layout(a, b);
   if (tid < 64) {
     const int r = blk * NC + tid;
     sm.colt[tid] = (unsigned char)min(r / a.G, a.T - 1);
@@ -650,11 +682,9 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     }
     if (tid < a.T) sm.mask[tid] = tree_mask(a, b, tid);
   }
-  if (NC < kOCols)                                    // columns of P that no row fills
-    for (int i = tid; i < 2 * kTT * 8; i += kThreads) reinterpret_cast<uint4*>(sm.P)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid < 256) {
-    const auto lev = [&](int k) { const int c = (tid >> (2 * k)) & 3; return c == 0 ? a.lev[0] : c == 1 ? a.lev[1] : c == 2 ? a.lev[2] : a.lev[3]; };
-    sm.lut[tid] = make_uint2(pack_half2(lev(0), lev(1)), pack_half2(lev(2), lev(3)));
+  if (tid >= 64 && tid < 80) {
+    const auto lev = [&](int c) { return c == 0 ? a.lev[0] : c == 1 ? a.lev[1] : c == 2 ? a.lev[2] : a.lev[3]; };
+    sm.lut[tid - 64] = pack_half2(lev(tid & 3), lev((tid - 64) >> 2));
   }
   const bool rotate = !tail && !a.naive;
   for (int c = warp; c < NC; c += kThreads / 32) {
@@ -781,7 +811,18 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       const uint32_t scol = tmem + lane_base + kSCol + bf * NC + c0;
       float2 p[8];
       uint32_t pk[8];
-      for (bool again = false;; again = true) {
+      // new references for the first tile and, rarely, later; then at most once
+      // (infinities may leave none)
+      for (bool renew = i == par, renewed = false;;) {
+        if (renew) {
+          renewed = true;
+          new_references(sm, a, scol, ocol, c0, par, i - PG, bar_id, rk, w, hidden);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            lacc[x].x *= sm.fl[par][c0 + 2 * x];
+            lacc[x].y *= sm.fl[par][c0 + 2 * x + 1];
+          }
+        }
         float pmax = 0.f, vmax = 0.f;
         uint32_t s[16];
         load_cols(scol, s);
@@ -820,15 +861,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
             pk[2 * y + z] = pack_half2(v.x, v.y);
           }
         }
-        // a second time only where infinities leave no reference
-        if (!bar_or(bar_id, 128, pmax > kSumLimit || vmax > kPLimit) || again) break;
-        // the first tile, and rarely after: new references for these rows
-        new_references(sm, a, scol, ocol, c0, par, i - PG, bar_id, rk, w, special ? vis : ~0ull);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          lacc[x].x *= sm.fl[par][c0 + 2 * x];
-          lacc[x].y *= sm.fl[par][c0 + 2 * x + 1];
-        }
+        renew = bar_or(bar_id, 128, pmax > kSumLimit || vmax > kPLimit);
+        if (!renew || renewed) break;
       }
 #pragma unroll
       for (int x = 0; x < 8; ++x) lacc[x] = __fadd2_rn(lacc[x], p[x]);
@@ -867,43 +901,46 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     // outputs in units of the sum's reference (of the larger, where two groups
     // have these rows; each writes half of them)
     tc::named_bar(8 + grp / PG, 128 * PG);
-    if (n > 1) wait_b(sm, &sm.pv[(n - 2) & 1], ((n - 2) >> 1) & 1, a);
-    wait_b(sm, &sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, a);
-    tc::fence_after_sync();
     const bool nan = *(volatile int*)&sm.err || *(volatile int*)&sm.bad;
     if (nan && tid == 0) latch_error(a.counters, kDevErrBounds);
-    float* o = a.part + (unit * a.parts + part) * NC * kD + tok;
-#pragma unroll 1
-    for (int x = c0 + par * (16 / PG); x < c0 + (par + 1) * (16 / PG); x += 8) {
-      uint32_t v[PG][8];
-#pragma unroll
-      for (int k = 0; k < PG; ++k) {
-        tmem_ld8(tmem + lane_base + k * kOCols + x, v[k]);
-        tmem_wait_ld8(v[k]);
-      }
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const int c = x + y;
-        const float m = PG == 2 ? fmaxf(-sm.nm[0][c], -sm.nm[1][c]) : -sm.nm[0][c];
-        float acc = 0.f;
-#pragma unroll
-        for (int k = 0; k < PG; ++k)
-          if (sm.nm[k][c] < INFINITY) acc = fmaf(__uint_as_float(v[k][y]), exp2f(sm.mp[k][c] - m), acc);
-        o[c * kD] = acc;
-      }
-    }
-    if (par == 0 && tok < 16) {
+    if (tok < 16) {
       const int c = c0 + tok;
       const float m = PG == 2 ? fmaxf(-sm.nm[0][c], -sm.nm[1][c]) : -sm.nm[0][c];
       float l = 0.f;
 #pragma unroll
       for (int k = 0; k < PG; ++k) {
         const float sum = sm.lsum[k][0][c] + sm.lsum[k][1][c] + sm.lsum[k][2][c] + sm.lsum[k][3][c];
+        const bool has = sm.nm[k][c] < INFINITY;
         // a sum without a reference is zero, or NaN
-        l += sm.nm[k][c] < INFINITY ? sum * exp2f(-sm.nm[k][c] - m) : sum;
+        l += has ? sum * pow2(-sm.nm[k][c] - m) : sum;
+        // each group for itself: the factor of its half's outputs of either parity
+        sm.fl[par][k * 16 + tok + c0 * PG] = has ? pow2(sm.mp[k][c] - m) : 0.f;
       }
-      ml[2 * c] = nan ? 0.f : m;
-      ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : l;
+      if (par == 0) {
+        ml[2 * c] = nan ? 0.f : m;
+        ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : l;
+      }
+    }
+    if (n > 1) wait_b(sm, &sm.pv[(n - 2) & 1], ((n - 2) >> 1) & 1, a);
+    wait_b(sm, &sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, a);
+    tc::fence_after_sync();
+    tc::named_bar(bar_id, 128);
+    const float* fo = &sm.fl[par][c0 * PG];
+    float* o = a.part + ((unit * a.parts + part) * NC + c0) * kD + tok;
+#pragma unroll 1
+    for (int x = par * (16 / PG); x < (par + 1) * (16 / PG); x += 4) {
+      uint32_t v[PG][4];
+#pragma unroll
+      for (int k = 0; k < PG; ++k) {
+        tmem_ld4(tmem + lane_base + k * kOCols + c0 + x, v[k]);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        // a parity without a reference has nothing (and, without a tile, no number) there
+        float acc = fo[x + y] != 0.f ? __uint_as_float(v[0][y]) * fo[x + y] : 0.f;
+        if (PG == 2 && fo[16 + x + y] != 0.f) acc = fmaf(__uint_as_float(v[PG - 1][y]), fo[16 + x + y], acc);
+        o[(x + y) * kD] = acc;
+      }
     }
     tc::fence_before_sync();
   }
@@ -912,63 +949,84 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   if (warp == kMma) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// One warp per output row: the parts joined by their references and sums, the
-// compressed tokens' share rotated back.  Bound by the parts' reads from L2.
+// Four warps per output row, each a quarter of the parts: joined by their
+// references and sums, the compressed tokens' share rotated back.  Bound by the
+// latency of the parts' reads from L2, so they are spread over warps.
 template <int NC>
 __global__ void __launch_bounds__(256) tree_tc_merge_kernel(TreeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  __shared__ float4 sum[2][4][2][32];
+  __shared__ float2 lm[2][4];
+  const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, grp = threadIdx.x >> 7;
+  const int64_t i = (int64_t)blockIdx.x * 2 + grp;
   const int Hq = a.H * a.G;
-  if (i >= (int64_t)a.batch * a.T * Hq) return;
-  const int b = (int)(i / (a.T * Hq)), t = (int)(i / Hq % a.T), hq = (int)(i % Hq), h = hq / a.G;
-  if (t >= tree_new(a, b)) return;
+  const bool there = i < (int64_t)a.batch * a.T * Hq;
+  const int b = there ? (int)(i / (a.T * Hq)) : 0, t = (int)(i / Hq % a.T), hq = (int)(i % Hq), h = hq / a.G;
+  if (!there || t >= tree_new(a, b)) return;
   const int r = t * a.G + hq % a.G;
   const int64_t unit = ((int64_t)b * a.H + h) * a.n_blk + r / NC;
   const float2* ml = reinterpret_cast<const float2*>(a.ml) + unit * a.parts * NC + r % NC;
   const float* o = a.part + (unit * a.parts * NC + r % NC) * kD + lane * 4;
-  float m = -INFINITY;
-  for (int s = lane; s < a.parts; s += 32) m = fmaxf(m, ml[(int64_t)s * NC].x);
-  m = warp_max(m);
-  float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+  // parts wq, wq + 4, ...: exact tokens' (y) and compressed tokens' (x) in units
+  // of the largest reference met so far
+  float m = -INFINITY, l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 4
-  for (int s = 0; s < a.parts; ++s) {
+  for (int s = wq; s < a.parts; s += 4) {
     const float2 e = ml[(int64_t)s * NC];
-    if (e.y == 0.f) continue;
-    const float w = exp2f(e.x - m);
     const float4 v = *reinterpret_cast<const float4*>(o + (int64_t)s * NC * kD);
-    l = fmaf(w, e.y, l);
-    float* z = s < a.tail_parts ? y : x;
-    z[0] = fmaf(w, v.x, z[0]);
-    z[1] = fmaf(w, v.y, z[1]);
-    z[2] = fmaf(w, v.z, z[2]);
-    z[3] = fmaf(w, v.w, z[3]);
+    if (e.y == 0.f) continue;
+    const float mn = fmaxf(m, e.x), f = m > -INFINITY ? exp2f(m - mn) : 0.f, g = exp2f(e.x - mn);
+    m = mn;
+    l = l * f + e.y * g;
+    x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+    y.x *= f; y.y *= f; y.z *= f; y.w *= f;
+    float4& z = s < a.tail_parts ? y : x;
+    z.x = fmaf(v.x, g, z.x); z.y = fmaf(v.y, g, z.y); z.z = fmaf(v.z, g, z.z); z.w = fmaf(v.w, g, z.w);
+  }
+  sum[grp][wq][0][lane] = x;
+  sum[grp][wq][1][lane] = y;
+  if (lane == 0) lm[grp][wq] = make_float2(m, l);
+  tc::named_bar(1 + grp, 128);
+  if (wq) return;
+  m = fmaxf(fmaxf(lm[grp][0].x, lm[grp][1].x), fmaxf(lm[grp][2].x, lm[grp][3].x));
+  float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 e = lm[grp][k];
+    if (e.y == 0.f) continue;
+    const float f = exp2f(e.x - m);
+    const float4 p = sum[grp][k][0][lane], q = sum[grp][k][1][lane];
+    l = fmaf(e.y, f, l);
+    c[0] = fmaf(p.x, f, c[0]); c[1] = fmaf(p.y, f, c[1]); c[2] = fmaf(p.z, f, c[2]); c[3] = fmaf(p.w, f, c[3]);
+    d[0] = fmaf(q.x, f, d[0]); d[1] = fmaf(q.y, f, d[1]); d[2] = fmaf(q.z, f, d[2]); d[3] = fmaf(q.w, f, d[3]);
   }
   if (!a.naive && a.comp) {
-    fwht128(x);
+    fwht128(c);
     const float n = rsqrtf((float)kD);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int d = 4 * lane + e;
-      x[e] *= (a.sign_bits[d >> 5] >> (d & 31)) & 1u ? -n : n;
+      const int k = 4 * lane + e;
+      c[e] *= (a.sign_bits[k >> 5] >> (k & 31)) & 1u ? -n : n;
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = (x[e] + y[e]) * inv;
+  for (int e = 0; e < 4; ++e) c[e] = (c[e] + d[e]) * inv;
   // infinities and NaN of the drafts' values, for the rows that see them
   unsigned long long odd = a.inf_v[(int64_t)b * a.H + h] & tree_mask(a, b, t);
   while (odd) {
-    const int d = __ffsll((long long)odd) - 1;
+    const int k = __ffsll((long long)odd) - 1;
     odd &= odd - 1;
     float v[4];
-    load4<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.vn) + b * a.n_seq + d * a.n_tok + h * kD + lane * 4, v);
+    load4<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.vn) + b * a.n_seq + k * a.n_tok + h * kD + lane * 4, v);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (!isfinite(v[e])) x[e] += v[e];
+      if (!isfinite(v[e])) c[e] += v[e];
   }
   // the one rounding to the output's type
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(c[0], c[1]), hi = __floats2bfloat162_rn(c[2], c[3]);
   reinterpret_cast<uint2*>(a.out)[i * 32 + lane] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
@@ -1014,7 +1072,7 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, s, a);
   if (st) return st;
   const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
-  return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 7) / 8)), 256, 0, s, a);
+  return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 1) / 2)), 256, 0, s, a);
 }
 
 }  // namespace
