@@ -56,15 +56,8 @@ namespace {
 
 constexpr int kTT = 128;                  // tokens of a tile
 constexpr int kSt = 2;                    // stages of the key and value rings
-// Token tables are loaded four tiles ahead, when the tile four before has been
-// multiplied; a key tile's scales are read up to two tiles after that.
-constexpr int kMetaSl = 4, kKSl = 8, kVSl = 4;
-constexpr int kCodeSl = 3;                // codes, three tiles ahead: they come from HBM
 constexpr int kTileBytes = kTT * kD * 2;
 constexpr int kHalf = kTileBytes / 2;     // 64 coordinates of every row
-constexpr int kOCols = 64;                // output columns in tensor memory, twice (even and odd tiles)
-constexpr int kSCol = 2 * kOCols;         // logits
-constexpr int kTmemCols = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 // A new reference puts the largest |w p| between 2^-6 and 2^-5: 20 bits below
 // the limit for later tiles, and what fp16 rounds away below 2^-14 is at most
@@ -90,35 +83,63 @@ struct Meta {
 };
 static_assert(sizeof(Table) % 16 == 0 && offsetof(Meta, table) % 16 == 0, "copied in 16-byte pieces");
 
+// What goes with NC, the rows (columns of the accumulators) of a CTA.
+template <int NC>
+struct Shape {
+  // Softmax groups of four warps have CW of the rows each and, where PG is 2,
+  // every other tile.  Sixteen rows a group were faster than 32 (16 drafts x 4
+  // heads behind 32 k tokens: 52.7 us, 60.4 with 32 rows and two parities)
+  // wherever the warps suffice.
+  static constexpr int CW = NC == 128 ? 32 : 16, CG = NC / CW, PG = NC == 16 ? 2 : 1, kGroups = CG * PG;
+  // Warps: softmax, the one that issues the MMAs, a loader of token tables for
+  // each side, producers.
+  static constexpr int kProd = NC <= 32 ? 16 : 8;
+  static constexpr int kMma = 4 * kGroups, kLoad = kMma + 1, kFirstProd = kMma + 3, kThreads = 32 * (kFirstProd + kProd);
+  // Tensor memory: outputs (of each parity), then two buffers of logits.
+  static constexpr int kOCols = NC < 64 ? 64 : NC, kSCol = PG * kOCols, kTmemCols = NC == 128 ? 512 : 256;
+  // Shared memory: buffers of P in blocks of 64 rows; token tables, loaded
+  // kMetaSl tiles ahead when the tile whose place they take has been
+  // multiplied, with value scales; key scales, which are read up to two tiles
+  // after that; codes, one tile less ahead (they come from HBM).
+  static constexpr int kPBuf = NC == 128 ? 1 : 2, kPBytes = kTT * 2 * kOCols;
+  static constexpr int kMetaSl = NC == 128 ? 3 : 4, kVSl = kMetaSl, kKSl = kMetaSl + 2, kCodeSl = kMetaSl - 1;
+};
+
+template <int NC>
 struct Sm {
+  using S = Shape<NC>;
+  static constexpr int kRows = S::kOCols;
   uint8_t K[kSt][kTileBytes];
   uint8_t V[kSt][kTileBytes];
-  uint8_t P[2][kTT * 128];                // [token][64 rows] fp16, swizzled
-  uint8_t Q[64 * kD * 2];
-  alignas(16) uint8_t codes[2][kCodeSl][kTT * kCodeBytes];        // [side]
-  alignas(16) Table meta[2][kMetaSl];     // [side]
-  alignas(16) float rk[kKSl][kTT];        // key scales
-  alignas(16) float wv[kVSl][kTT];        // value scales
+  uint8_t P[S::kPBuf][S::kPBytes];        // [64 rows][token][row] fp16, swizzled
+  uint8_t Q[NC * kD * 2];
+  alignas(16) uint8_t codes[2][S::kCodeSl][kTT * kCodeBytes];     // [side]
+  alignas(16) Table meta[2][S::kMetaSl];  // [side]
+  alignas(16) float rk[S::kKSl][kTT];     // key scales
+  alignas(16) float wv[S::kVSl][kTT];     // value scales
   uint32_t lut[16];                       // two codes -> their levels in fp16
-  uint64_t drain;                         // products after a failure
-  alignas(16) float cs[64];               // per row: logit scale
-  // per row, of the even and the odd tiles: -reference of the sum,
-  // 2^(reference of the sum - that of w p), reference of w p
-  alignas(16) float nm[2][64], cw[2][64], mp[2][64];
-  float fl[2][64];                        // rescaling of the sums; at the end of the outputs
-  int red[2][2][4][64];
-  float lsum[2][4][64];
+  alignas(16) float cs[kRows];            // per row: logit scale
+  // per row and tile parity: -reference of the sum, 2^(reference of the sum -
+  // that of w p), reference of w p
+  alignas(16) float nm[S::PG][kRows], cw[S::PG][kRows], mp[S::PG][kRows];
+  float fl[S::PG][kRows];                 // rescaling of the sums
+  int red[S::kGroups][2][4][16];          // maxima; factors of the outputs
+  float lsum[S::PG][4][kRows];
   unsigned long long mask[kTreeMaxDrafts];
-  unsigned char colt[64];                 // draft of each row
-  uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[kKSl], sv[kVSl];   // full: [side][stage]
-  uint64_t loaded[2][kMetaSl], coded[2][kCodeSl];     // token tables, codes
+  unsigned char colt[kRows];              // draft of each row
+  uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[S::kKSl], sv[S::kVSl];   // full: [side][stage]
+  uint64_t loaded[2][S::kMetaSl], coded[2][S::kCodeSl];     // token tables, codes
+  uint64_t drain;                         // products after a failure
   uint32_t tmem;
   int err, bad, rep;
 };
-static_assert(offsetof(Sm, cs) % 16 == 0 && offsetof(Sm, nm) % 16 == 0 && offsetof(Sm, cw) % 16 == 0 &&
-              offsetof(Sm, codes) % 16 == 0 && offsetof(Sm, meta) % 16 == 0 && offsetof(Sm, V) % 1024 == 0 && offsetof(Sm, P) % 1024 == 0 &&
-              offsetof(Sm, Q) % 1024 == 0, "16-byte reads, swizzle atoms");
-static_assert(kSt == 2, "the value ring and the P buffers share the barrier pv");
+template <int NC>
+constexpr bool sm_aligned() {
+  return offsetof(Sm<NC>, cs) % 16 == 0 && offsetof(Sm<NC>, nm) % 16 == 0 && offsetof(Sm<NC>, cw) % 16 == 0 &&
+         offsetof(Sm<NC>, codes) % 16 == 0 && offsetof(Sm<NC>, meta) % 16 == 0 && offsetof(Sm<NC>, V) % 1024 == 0 &&
+         offsetof(Sm<NC>, P) % 1024 == 0 && offsetof(Sm<NC>, Q) % 1024 == 0;
+}
+static_assert(sm_aligned<16>() && sm_aligned<32>() && sm_aligned<64>() && sm_aligned<128>(), "16-byte reads, swizzle atoms");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -306,7 +327,8 @@ __device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, int* err,
   if (*(volatile int*)err) return;
   tc::wait_or_fail(bar, parity, err, counters, kDevErrTimeout);
 }
-__device__ __forceinline__ void wait_b(Sm& sm, uint64_t* bar, uint32_t parity, const TreeArgs& a) {
+template <typename M>
+__device__ __forceinline__ void wait_b(M& sm, uint64_t* bar, uint32_t parity, const TreeArgs& a) {
   if (!tc::mbar_done(bar, parity)) wait_slow(bar, parity, &sm.err, a.counters);
 }
 
@@ -326,12 +348,19 @@ __device__ __forceinline__ Lane lane_of(int w) {
 
 // The stage of tile t is free: the products that read it last are done (keys:
 // the logits, values: the outputs).
-__device__ __forceinline__ void wait_free(Sm& sm, int side, int t, const TreeArgs& a) {
+template <typename M>
+__device__ __forceinline__ void wait_free(M& sm, int side, int t, const TreeArgs& a) {
   if (t >= 2) wait_b(sm, side ? &sm.pv[t & 1] : &sm.kempty[t & 1], ((t >> 1) - 1) & 1, a);
 }
 
-__device__ __forceinline__ float* scales_of(Sm& sm, int side, int t) { return side ? sm.wv[t % kVSl] : sm.rk[t % kKSl]; }
-__device__ __forceinline__ uint64_t* scales_bar(Sm& sm, int side, int t) { return side ? &sm.sv[t % kVSl] : &sm.sk[t % kKSl]; }
+template <typename M>
+__device__ __forceinline__ float* scales_of(M& sm, int side, int t) {
+  return side ? sm.wv[t % M::S::kVSl] : sm.rk[t % M::S::kKSl];
+}
+template <typename M>
+__device__ __forceinline__ uint64_t* scales_bar(M& sm, int side, int t) {
+  return side ? &sm.sv[t % M::S::kVSl] : &sm.sk[t % M::S::kKSl];
+}
 
 // x = ca x + cb level, two coordinates.
 __device__ __forceinline__ void add_levels(uint32_t& x, __half2 ca, __half2 cb, uint32_t level) {
@@ -339,13 +368,15 @@ __device__ __forceinline__ void add_levels(uint32_t& x, __half2 ca, __half2 cb, 
   x = *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Token tables and codes of one side, by one lane: tables four tiles ahead,
-// codes three.  Both are due when the tile four before the table's, whose
-// places they take, has been multiplied.
-__device__ void load_side(const TreeArgs& a, Sm& sm, int side, int n, const uint8_t* comp, const Meta* meta) {
+// Token tables and codes of one side, by one lane, as far ahead as there are
+// places: a place is free when the tile that had it has been multiplied.
+template <typename M>
+__device__ void load_side(const TreeArgs& a, M& sm, int side, int n, const uint8_t* comp, const Meta* meta) {
+  constexpr int kMetaSl = M::S::kMetaSl, kCodeSl = M::S::kCodeSl;
   const uint8_t* codes = comp + a.off_codes;
   for (int t = 0; t <= n; ++t) {
-    if (t >= 4) wait_b(sm, side ? &sm.pv[t & 1] : &sm.kempty[t & 1], ((t - 4) >> 1) & 1, a);
+    const int before = t - kMetaSl;
+    if (before >= 0) wait_b(sm, side ? &sm.pv[before & 1] : &sm.kempty[before & 1], (before >> 1) & 1, a);
     if (t < n) {
       uint64_t* mb = &sm.loaded[side][t % kMetaSl];
       tc::mbar_expect_tx(mb, sizeof(Table));
@@ -354,7 +385,7 @@ __device__ void load_side(const TreeArgs& a, Sm& sm, int side, int n, const uint
       tc::mbar_expect_tx(sb, kTT * 4);
       bulk_copy(tc::smem_u32(scales_of(sm, side, t)), meta[t].scale, kTT * 4, tc::smem_u32(sb));
     }
-    const int c = t - 1;
+    const int c = t - 1;                                           // takes the place of the codes of tile `before`
     if (c >= 0) {
       wait_b(sm, &sm.loaded[side][c % kMetaSl], (c / kMetaSl) & 1, a);
       const Table* m = &sm.meta[side][c % kMetaSl];
@@ -365,16 +396,17 @@ __device__ void load_side(const TreeArgs& a, Sm& sm, int side, int n, const uint
     }
   }
   // the copies are over before this CTA's shared memory is, also after a failure
-  for (int t = max(0, n - 4); t < n; ++t) {
+  for (int t = max(0, n - kMetaSl); t < n; ++t) {
     tc::mbar_wait(&sm.loaded[side][t % kMetaSl], (t / kMetaSl) & 1);
-    tc::mbar_wait(scales_bar(sm, side, t), (t / (side ? kVSl : kKSl)) & 1);
+    tc::mbar_wait(scales_bar(sm, side, t), (t / (side ? M::S::kVSl : M::S::kKSl)) & 1);
   }
   for (int t = max(0, n - kCodeSl); t < n; ++t) tc::mbar_wait(&sm.coded[side][t % kCodeSl], (t / kCodeSl) & 1);
 }
 
-template <int kProd>
-__device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const uint8_t* rows) {
-  const Lane me = lane_of<kProd>(w);
+template <typename M>
+__device__ void produce_prefix(const TreeArgs& a, M& sm, int w, int n, const uint8_t* rows) {
+  constexpr int kMetaSl = M::S::kMetaSl, kCodeSl = M::S::kCodeSl;
+  const Lane me = lane_of<M::S::kProd>(w);
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4, c8 = lane & 7, g = lane >> 3;
   rows += c * 16;
   for (int t = me.first; t < n; t += me.step) {
@@ -439,9 +471,9 @@ __device__ void produce_prefix(const TreeArgs& a, Sm& sm, int w, int n, const ui
 }
 
 // Exact rows, of pages and drafts: half a warp per row.
-template <int kProd>
-__device__ void produce_tail(const TreeArgs& a, Sm& sm, int w, int n, int b, int h, int tile0, int len, int n_new) {
-  const Lane me = lane_of<kProd>(w);
+template <typename M>
+__device__ void produce_tail(const TreeArgs& a, M& sm, int w, int n, int b, int h, int tile0, int len, int n_new) {
+  const Lane me = lane_of<M::S::kProd>(w);
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4;
   const uint16_t* pool = reinterpret_cast<const uint16_t*>(me.side ? a.vp : a.kp);
   const uint16_t* fresh = reinterpret_cast<const uint16_t*>(me.side ? a.vn : a.kn);
@@ -540,12 +572,30 @@ __device__ __noinline__ uint32_t hidden_columns(unsigned long long vis, const un
   return h;
 }
 
+// Sums over 16 lanes of 16 values a lane: lane l gets value l % 16 of its half.
+__device__ __forceinline__ float sum16(const float2 (&p)[8], int lane) {
+  float v[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) v[x] = x & 1 ? p[x / 2].y : p[x / 2].x;
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) {
+    const bool up = (lane & off) != 0;
+#pragma unroll
+    for (int x = 0; x < off; ++x) {
+      const float keep = up ? v[x + off] : v[x], send = up ? v[x] : v[x + off];
+      v[x] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+  }
+  return v[0];
+}
+
 // New references of rows c1 .. c1 + 15 for a softmax group whose last tile was
 // `before` (negative: none): the maxima over the tile's tokens, the factor of the sums so far (fl), and the
 // outputs so far in tensor memory.  Out of line and in loops: it runs once or
 // twice, and its code should not push the tile loops out of the instruction
 // caches.
-__device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t scol, uint32_t ocol, int c1, int par,
+template <typename M>
+__device__ __noinline__ void new_references(M& sm, const TreeArgs& a, uint32_t scol, uint32_t ocol, int c1, int par, int grp,
                                             int before, int bar_id, float rk, float w, uint32_t hidden) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, tok = threadIdx.x & 127;
   const float lw = w != 0.f ? __log2f(fabsf(w)) : -INFINITY;
@@ -562,18 +612,18 @@ __device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t 
       const int m1 = __reduce_max_sync(0xffffffffu, ordered(lg));
       const int m2 = __reduce_max_sync(0xffffffffu, ordered(lg + lw));
       if (lane == 0) {
-        sm.red[par][0][wq][c] = m1;
-        sm.red[par][1][wq][c] = m2;
+        sm.red[grp][0][wq][x + y] = m1;
+        sm.red[grp][1][wq][x + y] = m2;
       }
     }
   }
   tc::named_bar(bar_id, 128);
-  float* factor = reinterpret_cast<float*>(sm.red[par][0][0]) + c1;       // of the outputs, once the maxima are read
+  float* factor = reinterpret_cast<float*>(sm.red[grp][0][0]);             // of the outputs, once the maxima are read
   if (tok < 16) {
     const int c = c1 + tok;
-    const int(&r)[2][4][64] = sm.red[par];
-    const float m1 = unordered(max(max(r[0][0][c], r[0][1][c]), max(r[0][2][c], r[0][3][c])));
-    const float m2 = unordered(max(max(r[1][0][c], r[1][1][c]), max(r[1][2][c], r[1][3][c])));
+    const int(&r)[2][4][16] = sm.red[grp];
+    const float m1 = unordered(max(max(r[0][0][tok], r[0][1][tok]), max(r[0][2][tok], r[0][3][tok])));
+    const float m2 = unordered(max(max(r[1][0][tok], r[1][1][tok]), max(r[1][2][tok], r[1][3][tok])));
     const float l_old = -sm.nm[par][c], p_old = sm.mp[par][c];
     const float l_new = fmaxf(l_old, ceilf(m1));
     float p_new = fmaxf(p_old, ceilf(m2) + kPTarget);
@@ -602,21 +652,13 @@ __device__ __noinline__ void new_references(Sm& sm, const TreeArgs& a, uint32_t 
   }
 }
 
-// NC: rows (columns of the accumulators) of a CTA.  Softmax groups of four
-// warps have 16 of the rows each, and every tile or (PG = 2) every other tile;
-// then the warp that issues the MMAs, a loader of token tables for each side,
-// then the producers.
-template <int NC>
-struct Shape {
-  static constexpr int CG = NC / 16, PG = NC == 16 ? 2 : 1, kProd = NC == 64 ? 8 : 16;
-  static constexpr int kMma = 4 * CG * PG, kLoad = kMma + 1, kFirstProd = kMma + 3, kThreads = 32 * (kFirstProd + kProd);
-};
-
 template <int NC>
 __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArgs a) {
-  constexpr int CG = Shape<NC>::CG, PG = Shape<NC>::PG, kMma = Shape<NC>::kMma, kThreads = Shape<NC>::kThreads;
+  using S = Shape<NC>;
+  constexpr int CW = S::CW, CH = CW / 16, CG = S::CG, PG = S::PG, kMma = S::kMma, kThreads = S::kThreads;
+  constexpr int kOCols = S::kOCols, kSCol = S::kSCol, kKSl = S::kKSl, kVSl = S::kVSl;
   extern __shared__ __align__(1024) unsigned char raw[];
-  Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Sm<NC>& sm = *reinterpret_cast<Sm<NC>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int part = blockIdx.x, blk = blockIdx.y, bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
   const int64_t unit = (int64_t)bh * a.n_blk + blk;
@@ -646,7 +688,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
 
   // ---- set-up: barriers, tensor memory, queries, masks
   if (warp == kMma) {
-    tc::tmem_alloc(&sm.tmem, kTmemCols);
+    tc::tmem_alloc(&sm.tmem, S::kTmemCols);
     tc::tmem_relinquish();
   }
   if (warp == 0) {
@@ -654,8 +696,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     // arrival a warp
     if (lane < kKSl) tc::mbar_init(&sm.sk[lane], tail ? 4 : 1);
     if (lane < kVSl) tc::mbar_init(&sm.sv[lane], tail ? 4 : 1);
-    if (lane < 2 * kMetaSl) tc::mbar_init(&sm.loaded[0][0] + lane, 1);
-    if (lane < 2 * kCodeSl) tc::mbar_init(&sm.coded[0][0] + lane, 1);
+    if (lane < 2 * S::kMetaSl) tc::mbar_init(&sm.loaded[0][0] + lane, 1);
+    if (lane < 2 * S::kCodeSl) tc::mbar_init(&sm.coded[0][0] + lane, 1);
     if (lane < 4) tc::mbar_init(&sm.full[0][0] + lane, 4);
     if (lane < 2) {
       tc::mbar_init(&sm.kempty[lane], 1);
@@ -672,19 +714,19 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     tc::fence_barrier_init();
   }
   if (tid == 32) sm.rep = first_with_layout(a, b);
-  if (tid < 64) {
+  if (tid < kOCols) {
     const int r = blk * NC + tid;
     sm.colt[tid] = (unsigned char)min(r / a.G, a.T - 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < PG; ++i) {
       sm.nm[i][tid] = INFINITY;
       sm.mp[i][tid] = -INFINITY;
       sm.cw[i][tid] = 1.f;
     }
     if (tid < a.T) sm.mask[tid] = tree_mask(a, b, tid);
   }
-  if (tid >= 64 && tid < 80) {
+  if (tid >= 128 && tid < 144) {
     const auto lev = [&](int c) { return c == 0 ? a.lev[0] : c == 1 ? a.lev[1] : c == 2 ? a.lev[2] : a.lev[3]; };
-    sm.lut[tid - 64] = pack_half2(lev(tid & 3), lev((tid - 64) >> 2));
+    sm.lut[tid & 15] = pack_half2(lev(tid & 3), lev((tid >> 2) & 3));
   }
   const bool rotate = !tail && !a.naive;
   for (int c = warp; c < NC; c += kThreads / 32) {
@@ -718,15 +760,19 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = sm.tmem;
 
-  if (warp >= Shape<NC>::kFirstProd) {
+  if (warp >= S::kFirstProd) {
     // ---- rows of the key and value tiles
-    const int w = warp - Shape<NC>::kFirstProd;
-    if (tail) produce_tail<Shape<NC>::kProd>(a, sm, w, n, b, h, tile0, len, n_new);
-    else produce_prefix<Shape<NC>::kProd>(a, sm, w, n, reinterpret_cast<const uint8_t*>(a.anc) +
-                                                           (((int64_t)sm.rep * 2 + ((w >> 2) & 1)) * a.H + h) * a.k * (kD * 2));
+    const int w = warp - S::kFirstProd;
+    if (tail) {
+      produce_tail(a, sm, w, n, b, h, tile0, len, n_new);
+    } else {
+      const int64_t row0 = (((int64_t)sm.rep * 2 + ((w >> 2) & 1)) * a.H + h) * a.k;
+      produce_prefix(a, sm, w, n, reinterpret_cast<const uint8_t*>(a.anc) + row0 * (kD * 2));
+    }
   } else if (warp > kMma) {
+    // ---- token tables and codes
     if (!tail && lane == 0) {
-      const int side = warp - Shape<NC>::kLoad;
+      const int side = warp - S::kLoad;
       load_side(a, sm, side, n, a.comp + (int64_t)lay * a.stride,
                 reinterpret_cast<const Meta*>(a.meta) + (((int64_t)sm.rep * 2 + side) * a.H + h) * a.n_tiles + tile0);
     }
@@ -761,8 +807,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
           if (one && !*(volatile int*)&sm.err) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              mma_f16(tmem + (PG == 2 ? ob * kOCols : 0), vd, ob * kTileBytes + ks * 2048, pd, ob * (kTT * 128) + ks * 2048,
-                      id_o, o >= PG || ks > 0);
+              mma_f16(tmem + (PG == 2 ? ob * kOCols : 0), vd, ob * kTileBytes + ks * 2048, pd,
+                      (S::kPBuf == 2 ? ob * S::kPBytes : 0) + ks * 2048, id_o, o >= PG || ks > 0);
             tc::mma_commit(&sm.pv[ob]);
           }
         }
@@ -775,15 +821,22 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       __syncwarp();
     }
   } else {
-    // ---- softmax: thread = token; a group of four warps has 16 of the rows and,
+    // ---- softmax: thread = token; a group of four warps has CW of the rows and,
     // where two groups share them, every other tile with references, sums and
     // outputs of its own (par)
     const int tok = tid & 127, wq = warp & 3, grp = warp >> 2, par = PG == 2 ? grp & 1 : 0;
-    const int c0 = 16 * (grp / PG), bar_id = 1 + grp;
+    const int c0 = CW * (grp / PG), bar_id = 1 + grp;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16, ocol = tmem + lane_base + par * kOCols + c0;
+    // Sums: of 16 rows a register pair each and thread, added over the tokens at
+    // the end; of 32 rows added over 16 lanes in every tile (lane l: row l % 16),
+    // for which there are registers.
+    constexpr bool kWide = CH > 1;
     float2 lacc[8];
+    float lred[CH];
 #pragma unroll
     for (int x = 0; x < 8; ++x) lacc[x] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < CH; ++x) lred[x] = 0.f;
     for (int i = par; i < n; i += PG) {
       const int bf = i & 1;
       // what this token is, and who sees it
@@ -802,76 +855,92 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         live = t < a.N;
       }
       if (!live) vis = 0;
-      const uint32_t hidden = special ? hidden_columns(vis, &sm.colt[c0]) : 0u;
       wait_b(sm, &sm.sk[i % kKSl], (i / kKSl) & 1, a);
       wait_b(sm, &sm.sv[i % kVSl], (i / kVSl) & 1, a);
       const float rk = sm.rk[i % kKSl][tok], w = sm.wv[i % kVSl][tok];
       wait_b(sm, &sm.sfull[bf], (i >> 1) & 1, a);
       tc::fence_after_sync();
-      const uint32_t scol = tmem + lane_base + kSCol + bf * NC + c0;
-      float2 p[8];
-      uint32_t pk[8];
-      // new references for the first tile and, rarely, later; then at most once
-      // (infinities may leave none)
-      for (bool renew = i == par, renewed = false;;) {
-        if (renew) {
-          renewed = true;
-          new_references(sm, a, scol, ocol, c0, par, i - PG, bar_id, rk, w, hidden);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            lacc[x].x *= sm.fl[par][c0 + 2 * x];
-            lacc[x].y *= sm.fl[par][c0 + 2 * x + 1];
+      for (int ch = 0; ch < CH; ++ch) {
+        const int c1 = c0 + 16 * ch;
+        const uint32_t scol = tmem + lane_base + kSCol + bf * NC + c1;
+        const uint32_t hidden = special ? hidden_columns(vis, &sm.colt[c1]) : 0u;
+        float2 p[8];
+        uint32_t pk[8];
+        // new references for the first tile and, rarely, later; then at most once
+        // (infinities may leave none)
+        for (bool renew = i == par, renewed = false;;) {
+          if (renew) {
+            renewed = true;
+            new_references(sm, a, scol, ocol + 16 * ch, c1, par, grp, i - PG, bar_id, rk, w, hidden);
+            if (kWide) {
+              lred[ch] *= sm.fl[par][c1 + (lane & 15)];
+            } else {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                lacc[x].x *= sm.fl[par][c1 + 2 * x];
+                lacc[x].y *= sm.fl[par][c1 + 2 * x + 1];
+              }
+            }
           }
-        }
-        float pmax = 0.f, vmax = 0.f;
-        uint32_t s[16];
-        load_cols(scol, s);
-        float2 u[8];
+          float pmax = 0.f, vmax = 0.f;
+          uint32_t s[16];
+          load_cols(scol, s);
+          float2 u[8];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c0 + 4 * y]);
-          const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[par][c0 + 4 * y]);
+          for (int y = 0; y < 4; ++y) {
+            const float4 cs = *reinterpret_cast<const float4*>(&sm.cs[c1 + 4 * y]);
+            const float4 nm = *reinterpret_cast<const float4*>(&sm.nm[par][c1 + 4 * y]);
 #pragma unroll
-          for (int z = 0; z < 2; ++z)
-            u[2 * y + z] = __ffma2_rn(
-                make_float2(__uint_as_float(s[4 * y + 2 * z]), __uint_as_float(s[4 * y + 2 * z + 1])),
-                __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk)),
-                z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
-        }
-        if (hidden) {
-          asm volatile("");                    // a branch: ordinary tiles should not carry this as predicated instructions
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            if ((hidden >> (2 * x)) & 1u) u[x].x = -INFINITY;
-            if ((hidden >> (2 * x + 1)) & 1u) u[x].y = -INFINITY;
+            for (int z = 0; z < 2; ++z)
+              u[2 * y + z] = __ffma2_rn(
+                  make_float2(__uint_as_float(s[4 * y + 2 * z]), __uint_as_float(s[4 * y + 2 * z + 1])),
+                  __fmul2_rn(z ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y), make_float2(rk, rk)),
+                  z ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
           }
-        }
+          if (hidden) {
+            asm volatile("");                  // a branch: ordinary tiles should not carry this as predicated instructions
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[par][c0 + 4 * y]);
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const float2 e = make_float2(tc::ex2_approx(u[2 * y + z].x), tc::ex2_approx(u[2 * y + z].y));
-            // in this order a masked 0 stays 0 whatever the value's scale
-            const float2 v = __fmul2_rn(__fmul2_rn(e, make_float2(w, w)),
-                                        z ? make_float2(cw.z, cw.w) : make_float2(cw.x, cw.y));
-            pmax = fmaxf(pmax, fmaxf(e.x, e.y));
-            vmax = fmaxf(vmax, fmaxf(fabsf(v.x), fabsf(v.y)));
-            p[2 * y + z] = e;
-            pk[2 * y + z] = pack_half2(v.x, v.y);
+            for (int x = 0; x < 8; ++x) {
+              if ((hidden >> (2 * x)) & 1u) u[x].x = -INFINITY;
+              if ((hidden >> (2 * x + 1)) & 1u) u[x].y = -INFINITY;
+            }
           }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float4 cw = *reinterpret_cast<const float4*>(&sm.cw[par][c1 + 4 * y]);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float2 e = make_float2(tc::ex2_approx(u[2 * y + z].x), tc::ex2_approx(u[2 * y + z].y));
+              // in this order a masked 0 stays 0 whatever the value's scale
+              const float2 v = __fmul2_rn(__fmul2_rn(e, make_float2(w, w)),
+                                          z ? make_float2(cw.z, cw.w) : make_float2(cw.x, cw.y));
+              pmax = fmaxf(pmax, fmaxf(e.x, e.y));
+              vmax = fmaxf(vmax, fmaxf(fabsf(v.x), fabsf(v.y)));
+              p[2 * y + z] = e;
+              pk[2 * y + z] = pack_half2(v.x, v.y);
+            }
+          }
+          renew = bar_or(bar_id, 128, pmax > kSumLimit || vmax > kPLimit);
+          if (!renew || renewed) break;
         }
-        renew = bar_or(bar_id, 128, pmax > kSumLimit || vmax > kPLimit);
-        if (!renew || renewed) break;
+        if (ch == 0) {
+          // the products that read this buffer of P
+          constexpr int back = S::kPBuf;
+          if (i >= back) wait_b(sm, &sm.pv[(i - back) & 1], ((i - back) >> 1) & 1, a);
+        }
+        uint8_t* prow = sm.P[S::kPBuf == 2 ? bf : 0] + (c1 >> 6) * (kTT * 128) + tok * 128;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          *reinterpret_cast<uint4*>(prow + ((((c1 & 63) / 8 + x) ^ (tok & 7)) << 4)) =
+              make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+        if (kWide) {
+          lred[ch] += sum16(p, lane);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) lacc[x] = __fadd2_rn(lacc[x], p[x]);
+        }
       }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) lacc[x] = __fadd2_rn(lacc[x], p[x]);
-      if (i >= 2) wait_b(sm, &sm.pv[bf], ((i >> 1) - 1) & 1, a);   // the products that read this buffer of P
-      uint8_t* prow = sm.P[bf] + tok * 128;
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        *reinterpret_cast<uint4*>(prow + (((c0 / 8 + x) ^ (tok & 7)) << 4)) =
-            make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
@@ -882,39 +951,28 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- sums over the tokens
-    {
-      float v[16];
+    if (!kWide) lred[0] = sum16(lacc, lane);
 #pragma unroll
-      for (int x = 0; x < 16; ++x) v[x] = x & 1 ? lacc[x / 2].y : lacc[x / 2].x;
-#pragma unroll
-      for (int off = 8; off >= 1; off >>= 1) {       // lane l ends with column l % 16
-        const bool up = (lane & off) != 0;
-#pragma unroll
-        for (int x = 0; x < off; ++x) {
-          const float keep = up ? v[x + off] : v[x], send = up ? v[x] : v[x + off];
-          v[x] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-        }
-      }
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-      if (lane < 16) sm.lsum[par][wq][c0 + lane] = v[0];
+    for (int ch = 0; ch < CH; ++ch) {
+      const float l = lred[ch] + __shfl_xor_sync(0xffffffffu, lred[ch], 16);
+      if (lane < 16) sm.lsum[par][wq][c0 + 16 * ch + lane] = l;
     }
     // outputs in units of the sum's reference (of the larger, where two groups
     // have these rows; each writes half of them)
     tc::named_bar(8 + grp / PG, 128 * PG);
     const bool nan = *(volatile int*)&sm.err || *(volatile int*)&sm.bad;
     if (nan && tid == 0) latch_error(a.counters, kDevErrBounds);
-    if (tok < 16) {
+    float* fo = reinterpret_cast<float*>(sm.red[grp][0][0]);       // this group's factors of either parity's outputs
+    if (tok < CW) {
       const int c = c0 + tok;
-      const float m = PG == 2 ? fmaxf(-sm.nm[0][c], -sm.nm[1][c]) : -sm.nm[0][c];
+      const float m = PG == 2 ? fmaxf(-sm.nm[0][c], -sm.nm[PG - 1][c]) : -sm.nm[0][c];
       float l = 0.f;
 #pragma unroll
       for (int k = 0; k < PG; ++k) {
         const float sum = sm.lsum[k][0][c] + sm.lsum[k][1][c] + sm.lsum[k][2][c] + sm.lsum[k][3][c];
         const bool has = sm.nm[k][c] < INFINITY;
-        // a sum without a reference is zero, or NaN
-        l += has ? sum * pow2(-sm.nm[k][c] - m) : sum;
-        // each group for itself: the factor of its half's outputs of either parity
-        sm.fl[par][k * 16 + tok + c0 * PG] = has ? pow2(sm.mp[k][c] - m) : 0.f;
+        l += has ? sum * pow2(-sm.nm[k][c] - m) : sum;             // a sum without a reference is zero, or NaN
+        fo[k * 32 + tok] = has ? pow2(sm.mp[k][c] - m) : 0.f;
       }
       if (par == 0) {
         ml[2 * c] = nan ? 0.f : m;
@@ -925,20 +983,17 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     wait_b(sm, &sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, a);
     tc::fence_after_sync();
     tc::named_bar(bar_id, 128);
-    const float* fo = &sm.fl[par][c0 * PG];
     float* o = a.part + ((unit * a.parts + part) * NC + c0) * kD + tok;
 #pragma unroll 1
-    for (int x = par * (16 / PG); x < (par + 1) * (16 / PG); x += 4) {
+    for (int x = par * (CW / PG); x < (par + 1) * (CW / PG); x += 4) {
       uint32_t v[PG][4];
 #pragma unroll
-      for (int k = 0; k < PG; ++k) {
-        tmem_ld4(tmem + lane_base + k * kOCols + c0 + x, v[k]);
-      }
+      for (int k = 0; k < PG; ++k) tmem_ld4(tmem + lane_base + k * kOCols + c0 + x, v[k]);
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         // a parity without a reference has nothing (and, without a tile, no number) there
         float acc = fo[x + y] != 0.f ? __uint_as_float(v[0][y]) * fo[x + y] : 0.f;
-        if (PG == 2 && fo[16 + x + y] != 0.f) acc = fmaf(__uint_as_float(v[PG - 1][y]), fo[16 + x + y], acc);
+        if (PG == 2 && fo[32 + x + y] != 0.f) acc = fmaf(__uint_as_float(v[PG - 1][y]), fo[32 + x + y], acc);
         o[(x + y) * kD] = acc;
       }
     }
@@ -946,7 +1001,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   }
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == kMma) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMma) tc::tmem_dealloc(tmem, S::kTmemCols);
 }
 
 // Four warps per output row, each a quarter of the parts: joined by their
@@ -1046,8 +1101,11 @@ int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t s,
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ANCHORKV_OK : ANCHORKV_ECUDA;
 }
 
-constexpr int kSmem = (int)sizeof(Sm) + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+template <int NC>
+constexpr int smem_bytes() {
+  static_assert(sizeof(Sm<NC>) + 1024 <= 227 * 1024, "shared memory of one CTA");
+  return (int)sizeof(Sm<NC>) + 1024;
+}
 
 template <int NC>
 int launch_nc(const TreeArgs& a, cudaStream_t s) {
@@ -1058,7 +1116,7 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (ready_dev != dev) {
-      if (cudaFuncSetAttribute(tree_tc_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+      if (cudaFuncSetAttribute(tree_tc_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC>()) != cudaSuccess)
         return ANCHORKV_ECUDA;
       ready_dev = dev;
     }
@@ -1069,7 +1127,7 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   int st = ANCHORKV_OK;
   if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 1) / 2, 2 * a.H, a.batch), 256, 0, s, a);
   if (st) return st;
-  st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, kSmem, s, a);
+  st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, smem_bytes<NC>(), s, a);
   if (st) return st;
   const int64_t rows = (int64_t)a.batch * a.T * a.H * a.G;
   return launch_dependent(tree_tc_merge_kernel<NC>, dim3((unsigned)((rows + 1) / 2)), 256, 0, s, a);
@@ -1080,29 +1138,33 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
 int64_t tree_meta_bytes() { return (int64_t)sizeof(Meta); }
 
 void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
-  tp->RB = tp->rows <= 16 ? 16 : tp->rows <= 32 ? 32 : 64;
-  tp->n_blk = (tp->rows + tp->RB - 1) / tp->RB;
-  const int64_t units = (int64_t)tp->batch * pl.H * tp->n_blk;
-  const int64_t pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (tp->cap + tp->T + kTT - 1) / kTT;
   // One CTA an SM.  A CTA costs about kFixed tiles beside its own (set-up,
-  // first reference, outputs), so the split is the one whose longest run of
-  // CTAs on an SM is shortest.
-  constexpr int64_t kFixed = 4;
+  // first references, outputs) and a tile of 16, 32, 64 or 128 rows the times
+  // below (in tenths of a microsecond, measured over 32 k and 128 k tokens), so
+  // the block and the split are those whose longest run of CTAs on an SM is
+  // shortest.
+  constexpr int64_t kFixed = 6;
+  constexpr int kRows[4] = {16, 32, 64, 128}, kTime[4] = {12, 14, 17, 29};
+  const int64_t pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (tp->cap + tp->T + kTT - 1) / kTT;
   int64_t best = INT64_MAX;
-  tp->parts = tp->tail_parts = 1;
-  for (int64_t s = prefix ? 1 : 0; s <= std::min<int64_t>(pre, 148); ++s) {
-    const int64_t per = s ? (pre + s - 1) / s : 8, t = (tail + std::max<int64_t>(per, 4) - 1) / std::max<int64_t>(per, 4);
-    const int64_t waves = (units * (s + t) + 147) / 148, cost = waves * (per + kFixed);
-    if (cost < best) {
-      best = cost;
-      tp->parts = (int)(s + t);
-      tp->tail_parts = (int)t;
+  for (int k = 0; k < 4; ++k) {
+    const int64_t n_blk = (tp->rows + kRows[k] - 1) / kRows[k], units = (int64_t)tp->batch * pl.H * n_blk;
+    for (int64_t s = prefix ? 1 : 0; s <= std::min<int64_t>(pre, 148); ++s) {
+      const int64_t per = s ? (pre + s - 1) / s : 8, t = (tail + std::max<int64_t>(per, 4) - 1) / std::max<int64_t>(per, 4);
+      const int64_t waves = (units * (s + t) + 147) / 148, cost = waves * (per + kFixed) * kTime[k];
+      if (cost < best) {
+        best = cost;
+        tp->RB = kRows[k];
+        tp->n_blk = (int)n_blk;
+        tp->parts = (int)(s + t);
+        tp->tail_parts = (int)t;
+      }
     }
   }
 }
 
 int launch_tree_tc(const TreeArgs& a, cudaStream_t s) {
-  return a.RB == 16 ? launch_nc<16>(a, s) : a.RB == 32 ? launch_nc<32>(a, s) : launch_nc<64>(a, s);
+  return a.RB == 16 ? launch_nc<16>(a, s) : a.RB == 32 ? launch_nc<32>(a, s) : a.RB == 64 ? launch_nc<64>(a, s) : launch_nc<128>(a, s);
 }
 
 }  // namespace akv
