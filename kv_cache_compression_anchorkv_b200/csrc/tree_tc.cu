@@ -91,10 +91,10 @@ struct Shape {
   // heads behind 32 k tokens: 52.7 us, 60.4 with 32 rows and two parities)
   // wherever the warps suffice.
   static constexpr int CW = NC == 128 ? 32 : 16, CG = NC / CW, PG = NC == 16 ? 2 : 1, kGroups = CG * PG;
-  // Warps: softmax, the one that issues the MMAs, a loader of token tables for
-  // each side, producers.
+  // Warps: softmax, one that issues the logits' MMAs and one the outputs', a
+  // loader of token tables for each side, producers.
   static constexpr int kProd = NC <= 32 ? 16 : 8;
-  static constexpr int kMma = 4 * kGroups, kLoad = kMma + 1, kFirstProd = kMma + 3, kThreads = 32 * (kFirstProd + kProd);
+  static constexpr int kMma = 4 * kGroups, kLoad = kMma + 2, kFirstProd = kMma + 4, kThreads = 32 * (kFirstProd + kProd);
   // Tensor memory: outputs (of each parity), then two buffers of logits.
   static constexpr int kOCols = NC < 64 ? 64 : NC, kSCol = PG * kOCols, kTmemCols = NC == 128 ? 512 : 256;
   // Shared memory: buffers of P in blocks of 64 rows; token tables, loaded
@@ -129,7 +129,6 @@ struct Sm {
   unsigned char colt[kRows];              // draft of each row
   uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[S::kKSl], sv[S::kVSl];   // full: [side][stage]
   uint64_t loaded[2][S::kMetaSl], coded[2][S::kCodeSl];     // token tables, codes
-  uint64_t drain;                         // products after a failure
   uint32_t tmem;
   int err, bad, rep;
 };
@@ -181,13 +180,6 @@ __device__ __forceinline__ uint32_t bar_or(int id, int count, bool p) {
   return r;
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -209,17 +201,44 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_m
          ((uint32_t)(M >> 4) << 24);
 }
 
-// One MMA of fp16 operands whose descriptors differ from a tile's first only in
-// their low words.
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint32_t a_off, uint64_t b, uint32_t b_off, uint32_t idesc,
-                                        bool accumulate) {
+// The eight MMAs (K = 16 each) of one product of fp16 operands, issued by one
+// elected lane of a converged warp.  Elected
+// inside, so that the warp does not diverge and the descriptors stay in uniform
+// registers.  A0, A1, B0, B1: descriptor steps, in 16-byte units, from one MMA
+// to the next and from the fourth to the fifth.
+template <int A0, int A1, int B0, int B1>
+__device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}"
-      ::"r"(d), "r"((uint32_t)a + (a_off >> 4)), "r"((uint32_t)(a >> 32)), "r"((uint32_t)b + (b_off >> 4)),
-        "r"((uint32_t)(b >> 32)), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p, q, r;\n\t.reg .b64 x, y;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 r, 0, 0;\n\t"
+      "mov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "add.u64 x, x, %5;\n\tadd.u64 y, y, %7;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, r;\n\t"
+      "add.u64 x, x, %5;\n\tadd.u64 y, y, %7;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, r;\n\t"
+      "add.u64 x, x, %5;\n\tadd.u64 y, y, %7;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, r;\n\t"
+      "add.u64 x, x, %6;\n\tadd.u64 y, y, %8;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, r;\n\t"
+      "add.u64 x, x, %5;\n\tadd.u64 y, y, %7;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, r;\n\t"
+      "add.u64 x, x, %5;\n\tadd.u64 y, y, %7;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, r;\n\t"
+      "add.u64 x, x, %5;\n\tadd.u64 y, y, %7;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, r;\n\t"
+      "}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(A0), "n"(A1), "n"(B0), "n"(B1)
+      : "memory");
+}
+// The arrival on `bar` when they are done, by the same lane (the election of a
+// full warp is deterministic).
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(tc::smem_u32(bar))
       : "memory");
 }
 
@@ -707,7 +726,6 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       tc::mbar_init(&sm.pfull[lane], 4 * CG);
     }
     if (lane == 0) {
-      tc::mbar_init(&sm.drain, 1);
       sm.err = 0;
       sm.bad = 0;
     }
@@ -769,7 +787,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       const int64_t row0 = (((int64_t)sm.rep * 2 + ((w >> 2) & 1)) * a.H + h) * a.k;
       produce_prefix(a, sm, w, n, reinterpret_cast<const uint8_t*>(a.anc) + row0 * (kD * 2));
     }
-  } else if (warp > kMma) {
+  } else if (warp >= S::kLoad) {
     // ---- token tables and codes
     if (!tail && lane == 0) {
       const int side = warp - S::kLoad;
@@ -778,48 +796,34 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     }
     __syncwarp();
   } else if (warp == kMma) {
-    {
-      // ---- MMA issue
-      const bool one = elect_one();
-      constexpr uint32_t id_s = idesc_f16(128, NC, 0, 0), id_o = idesc_f16(128, kOCols, 1, 1);
-      const uint64_t kd = tc::sw128_desc(tc::smem_u32(sm.K)), qd = tc::sw128_desc(tc::smem_u32(sm.Q));
-      const uint64_t vd = tc::sw128_mn_desc(tc::smem_u32(sm.V), kHalf), pd = tc::sw128_mn_desc(tc::smem_u32(sm.P), kTT * 128);
-      for (int i = 0; i <= n; ++i) {
-        const int bf = i & 1;
-        if (i < n) {
-          wait_b(sm, &sm.full[0][bf], (i >> 1) & 1, a);
-          if (i >= 2) wait_b(sm, &sm.sempty[bf], ((i >> 1) - 1) & 1, a);
-          tc::fence_after_sync();
-          if (one && !*(volatile int*)&sm.err) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_f16(tmem + kSCol + bf * NC, kd, bf * kTileBytes + (ks >> 2) * kHalf + (ks & 3) * 32, qd,
-                      (ks >> 2) * (NC * 128) + (ks & 3) * 32, id_s, ks > 0);
-            tc::mma_commit(&sm.kempty[bf]);
-            tc::mma_commit(&sm.sfull[bf]);
-          }
-        }
-        if (i > 0) {
-          const int o = i - 1, ob = o & 1;
-          wait_b(sm, &sm.full[1][ob], (o >> 1) & 1, a);
-          wait_b(sm, &sm.pfull[ob], (o >> 1) & 1, a);
-          tc::fence_after_sync();
-          if (one && !*(volatile int*)&sm.err) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_f16(tmem + (PG == 2 ? ob * kOCols : 0), vd, ob * kTileBytes + ks * 2048, pd,
-                      (S::kPBuf == 2 ? ob * S::kPBytes : 0) + ks * 2048, id_o, o >= PG || ks > 0);
-            tc::mma_commit(&sm.pv[ob]);
-          }
-        }
-      }
-      // after a failure nobody waits for the products in flight: do it here
-      if (*(volatile int*)&sm.err) {
-        if (one) tc::mma_commit(&sm.drain);
-        tc::mbar_wait(&sm.drain, 0);
-      }
+    // ---- logits: S^T = K^ Q^T.  After a failed wait the products go on with
+    // whatever is there; the outputs become NaN at the end.
+    const uint64_t kd = tc::sw128_desc(tc::smem_u32(sm.K)), qd = tc::sw128_desc(tc::smem_u32(sm.Q));
+    for (int i = 0; i < n; ++i) {
+      const int bf = i & 1;
+      wait_b(sm, &sm.full[0][bf], (i >> 1) & 1, a);
+      if (i >= 2) wait_b(sm, &sm.sempty[bf], ((i >> 1) - 1) & 1, a);
       __syncwarp();
+      tc::fence_after_sync();
+      mma_tile<2, kHalf / 16 - 6, 2, NC * 8 - 6>(tmem + kSCol + bf * NC, kd + bf * (kTileBytes / 16), qd, idesc_f16(128, NC, 0, 0), 0);
+      commit_elected(&sm.kempty[bf]);
+      commit_elected(&sm.sfull[bf]);
     }
+    tc::mbar_wait(&sm.sfull[(n - 1) & 1], ((n - 1) >> 1) & 1);     // in every case over before the memory is freed
+  } else if (warp == kMma + 1) {
+    // ---- outputs: O^T += V^T P
+    const uint64_t vd = tc::sw128_mn_desc(tc::smem_u32(sm.V), kHalf), pd = tc::sw128_mn_desc(tc::smem_u32(sm.P), kTT * 128);
+    for (int i = 0; i < n; ++i) {
+      const int bf = i & 1;
+      wait_b(sm, &sm.full[1][bf], (i >> 1) & 1, a);
+      wait_b(sm, &sm.pfull[bf], (i >> 1) & 1, a);
+      __syncwarp();
+      tc::fence_after_sync();
+      mma_tile<128, 128, 128, 128>(tmem + (PG == 2 ? bf * kOCols : 0), vd + bf * (kTileBytes / 16),
+                                   pd + (S::kPBuf == 2 ? bf * (S::kPBytes / 16) : 0), idesc_f16(128, kOCols, 1, 1), i >= PG);
+      commit_elected(&sm.pv[bf]);
+    }
+    tc::mbar_wait(&sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1);
   } else {
     // ---- softmax: thread = token; a group of four warps has CW of the rows and,
     // where two groups share them, every other tile with references, sums and
