@@ -81,7 +81,7 @@ struct Meta {
   float scale[kTT];
   Table table;
 };
-static_assert(sizeof(Table) % 16 == 0 && offsetof(Meta, table) % 16 == 0, "copied in 16-byte pieces");
+static_assert(sizeof(Table) % 16 == 0 && offsetof(Table, quarter) % 16 == 0 && offsetof(Meta, table) % 16 == 0, "copied in 16-byte pieces");
 
 // What goes with NC, the rows (columns of the accumulators) of a CTA.
 template <int NC>
@@ -125,7 +125,7 @@ struct Sm {
   float fl[S::PG][kRows];                 // rescaling of the sums
   int red[S::kGroups][2][4][16];          // maxima; factors of the outputs
   float lsum[S::PG][4][kRows];
-  unsigned long long mask[kTreeMaxDrafts];
+  uint2 seen[kTreeMaxDrafts];             // of each draft, the drafts that see it
   unsigned char colt[kRows];              // draft of each row
   uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[S::kKSl], sv[S::kVSl];   // full: [side][stage]
   uint64_t loaded[2][S::kMetaSl], coded[2][S::kCodeSl];     // token tables, codes
@@ -297,46 +297,71 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
 // (2 KB a tile and side).
 __global__ void __launch_bounds__(256) tree_meta_kernel(TreeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kTiles = 2;                              // a warp's tiles, their loads in flight together
   const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, b = blockIdx.z, sh = blockIdx.y;
-  const int tile = blockIdx.x * 2 + (threadIdx.x >> 7), t = tile * kTT + q * 32 + lane;
-  if (tile >= a.n_tiles || first_with_layout(a, b) != b) return;
+  if (first_with_layout(a, b) != b) return;
   const int lay = tree_layout(a, b);
   if (lay < 0) return;
   const uint8_t* comp = a.comp + (int64_t)lay * a.stride;
-  const uint32_t word = t < a.N ? reinterpret_cast<const uint32_t*>(comp + a.off_tok)[(int64_t)sh * a.N + t] : 0u;
-  const uint4 bm = *reinterpret_cast<const uint4*>(comp + a.off_bm + ((int64_t)sh * a.n_tiles + tile) * 16);
-  const int first = reinterpret_cast<const int*>(comp + a.off_pf)[(int64_t)sh * (a.n_tiles + 1) + tile];
-  // bits behind the last token mean nothing, records outside the layout are none
-  uint32_t bits[4] = {bm.x, bm.y, bm.z, bm.w};
-  int before[5] = {0};
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(comp + a.off_tok) + (int64_t)sh * a.N;
+  const uint4* bms = reinterpret_cast<const uint4*>(comp + a.off_bm) + (int64_t)sh * a.n_tiles;
+  const int* pfs = reinterpret_cast<const int*>(comp + a.off_pf) + (int64_t)sh * (a.n_tiles + 1);
+  const uint16_t* sig = reinterpret_cast<const uint16_t*>(comp + a.off_sig);
+  const int tile0 = (blockIdx.x * 2 + (threadIdx.x >> 7)) * kTiles;
+  uint32_t word[kTiles];
+  uint4 bm[kTiles];
+  int first[kTiles];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int left = a.N - (tile * kTT + k * 32);
-    if (left < 32) bits[k] &= left > 0 ? (1u << left) - 1u : 0u;
-    before[k + 1] = before[k] + __popc(bits[k]);
+  for (int k = 0; k < kTiles; ++k) {
+    const int tile = tile0 + k, t = tile * kTT + q * 32 + lane;
+    word[k] = t < a.N ? words[t] : 0u;
+    bm[k] = tile < a.n_tiles ? bms[tile] : make_uint4(0u, 0u, 0u, 0u);
+    first[k] = tile < a.n_tiles ? pfs[tile] : 0;
   }
-  const bool fine = first >= 0 && first + (int64_t)before[4] <= a.R;
-  const uint32_t mine = q == 0 ? bits[0] : q == 1 ? bits[1] : q == 2 ? bits[2] : bits[3];
-  const int x = (q == 0 ? 0 : q == 1 ? before[1] : q == 2 ? before[2] : before[3]) + __popc(mine & ((1u << lane) - 1u));
-  const bool res = fine && ((mine >> lane) & 1u);
-  const int slot = min((int)(word & 0xffffu), a.k - 1);
-  const int64_t row0 = ((int64_t)b * 2 * a.H + sh) * a.k;
-  const float sg = res ? half_bits_to_f(reinterpret_cast<const uint16_t*>(comp + a.off_sig)[first + x]) : 0.f;
+  float sg[kTiles];
+  int x[kTiles], before[kTiles][4];
+  bool res[kTiles], fine[kTiles];
+#pragma unroll
+  for (int k = 0; k < kTiles; ++k) {
+    // bits behind the last token mean nothing, records outside the layout are none
+    uint32_t bits[4] = {bm[k].x, bm[k].y, bm[k].z, bm[k].w};
+    const int left = a.N - (tile0 + k) * kTT;
+    int sum = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      if (left < 32 * y + 32) bits[y] &= left > 32 * y ? (1u << (left - 32 * y)) - 1u : 0u;
+      sum += __popc(bits[y]);
+      before[k][y] = sum;
+    }
+    fine[k] = first[k] >= 0 && first[k] + (int64_t)sum <= a.R;
+    const uint32_t mine = q == 0 ? bits[0] : q == 1 ? bits[1] : q == 2 ? bits[2] : bits[3];
+    x[k] = (q == 0 ? 0 : q == 1 ? before[k][0] : q == 2 ? before[k][1] : before[k][2]) + __popc(mine & ((1u << lane) - 1u));
+    res[k] = fine[k] && ((mine >> lane) & 1u);
+    sg[k] = res[k] ? half_bits_to_f(sig[first[k] + x[k]]) : 0.f;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float c1 = half_bits_to_f(word >> 16) * a.anc_scale[row0 + slot];
-  const float sc = fabsf(c1) >= sg ? c1 : sg, inv = sc != 0.f ? 1.f / sc : 0.f;
-  Meta* m = reinterpret_cast<Meta*>(a.meta) + ((int64_t)b * 2 * a.H + sh) * a.n_tiles + tile;
-  m->scale[q * 32 + lane] = sc;                          // 0 behind the last token, whose word is 0
-  m->table.slot[q * 32 + lane] = (uint16_t)slot;
-  if (res) {
-    m->table.fac[x] = pack_half2(c1 * inv, sg * inv);
-    m->table.tok[x] = (uint8_t)(q * 32 + lane);
-  }
-  if (q == 0 && lane == 0) {
-    m->table.quarter = fine ? (uint32_t)before[1] << 8 | (uint32_t)before[2] << 16 | (uint32_t)before[3] << 24 : 0u;
-    m->table.n_rec = fine ? (uint32_t)before[4] : 0u;
-    m->table.first = fine ? (uint32_t)first : 0u;
-    m->table.pad = 0u;
+  const float* scale = a.anc_scale + ((int64_t)b * 2 * a.H + sh) * a.k;
+  float m[kTiles];
+#pragma unroll
+  for (int k = 0; k < kTiles; ++k) m[k] = scale[min((int)(word[k] & 0xffffu), a.k - 1)];
+  Meta* out = reinterpret_cast<Meta*>(a.meta) + ((int64_t)b * 2 * a.H + sh) * a.n_tiles;
+#pragma unroll
+  for (int k = 0; k < kTiles; ++k) {
+    if (tile0 + k >= a.n_tiles) break;
+    Meta& o = out[tile0 + k];
+    const float c1 = half_bits_to_f(word[k] >> 16) * m[k];
+    const float sc = fabsf(c1) >= sg[k] ? c1 : sg[k], inv = sc != 0.f ? __fdividef(1.f, sc) : 0.f;
+    o.scale[q * 32 + lane] = sc;                         // 0 behind the last token, whose word is 0
+    o.table.slot[q * 32 + lane] = (uint16_t)min((int)(word[k] & 0xffffu), a.k - 1);
+    if (res[k]) {
+      o.table.fac[x[k]] = pack_half2(c1 * inv, sg[k] * inv);
+      o.table.tok[x[k]] = (uint8_t)(q * 32 + lane);
+    }
+    if (q == 0 && lane == 0) {
+      const uint32_t* f = reinterpret_cast<const uint32_t*>(before[k]);
+      *reinterpret_cast<uint4*>(&o.table.quarter) =
+          fine[k] ? make_uint4(f[0] << 8 | f[1] << 16 | f[2] << 24, f[3], (uint32_t)first[k], 0u) : make_uint4(0u, 0u, 0u, 0u);
+    }
   }
 }
 
@@ -489,64 +514,78 @@ __device__ void produce_prefix(const TreeArgs& a, M& sm, int w, int n, const uin
   }
 }
 
-// Exact rows, of pages and drafts: half a warp per row.
+// Exact rows, of pages and drafts: half a warp per row, the rows' addresses
+// found by one lane each beforehand.
 template <typename M>
 __device__ void produce_tail(const TreeArgs& a, M& sm, int w, int n, int b, int h, int tile0, int len, int n_new) {
   const Lane me = lane_of<M::S::kProd>(w);
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4;
   const uint16_t* pool = reinterpret_cast<const uint16_t*>(me.side ? a.vp : a.kp);
   const uint16_t* fresh = reinterpret_cast<const uint16_t*>(me.side ? a.vn : a.kn);
+  const int* table = a.table + (int64_t)b * a.maxp;
   for (int tl = me.first; tl < n; tl += me.step) {
+    const int first = (tile0 + tl) * kTT + me.q * 32;              // this warp's first token
+    unsigned long long at = 0;                                     // lane l: row of token first + l, or none
+    {
+      const int t = first + lane;
+      if (t < len) {
+        const int pg = table[t / a.P];
+        if (pg >= 0 && pg < a.n_pages)
+          at = (unsigned long long)(pool + (((int64_t)pg * a.H + h) * a.P + t % a.P) * kD);
+        else
+          *(volatile int*)&sm.bad = 1;
+      } else if (t - len < n_new) {
+        at = (unsigned long long)(fresh + b * a.n_seq + (int64_t)(t - len) * a.n_tok + h * kD);
+      }
+    }
     wait_free(sm, me.side, tl, a);
     uint8_t* tile = me.side ? sm.V[tl & 1] : sm.K[tl & 1];
-    const int first = (tile0 + tl) * kTT;
-    for (int r0 = me.q * 32 + hw; r0 < me.q * 32 + 32; r0 += 8) {
+    float* scales = scales_of(sm, me.side, tl) + me.q * 32;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8) {                           // this half's rows r0 + 2 k + hw
       uint4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int t = first + r0 + 2 * k;
-        v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (t < len) {
-          const int pg = a.table[(int64_t)b * a.maxp + t / a.P];
-          if (pg >= 0 && pg < a.n_pages)
-            v[k] = *reinterpret_cast<const uint4*>(pool + (((int64_t)pg * a.H + h) * a.P + t % a.P) * kD + c * 8);
-          else
-            *(volatile int*)&sm.bad = 1;
-        } else if (t - len < n_new) {
-          v[k] = *reinterpret_cast<const uint4*>(fresh + b * a.n_seq + (int64_t)(t - len) * a.n_tok + h * kD + c * 8);
-        }
+        const unsigned long long p = __shfl_sync(0xffffffffu, at, r0 + 2 * k + hw);
+        v[k] = p ? reinterpret_cast<const uint4*>(p)[c] : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int r = r0 + 2 * k, t = first + r;
-        const uint32_t* vw = reinterpret_cast<const uint32_t*>(&v[k]);
-        float x[8];
+        const int r = r0 + 2 * k + hw;
+        uint32_t* vw = reinterpret_cast<uint32_t*>(&v[k]);
+        uint32_t m2 = 0;                                           // magnitudes as 15-bit integers, two at a time
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          x[2 * y] = __uint_as_float(vw[y] << 16);
-          x[2 * y + 1] = __uint_as_float(vw[y] & 0xffff0000u);
-        }
-        uint32_t m = 0;
-        bool odd = false;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const uint32_t bits = __float_as_uint(x[y]) & 0x7fffffffu;
-          const bool fin = bits < 0x7f800000u;
-          if (fin) m = max(m, bits);
-          odd = odd || !fin;
-          // an infinity or NaN in a draft's value must not reach the rows that
-          // do not see it (0 x inf): the merge adds it where it is seen
-          if (!fin && me.side && t >= len) x[y] = 0.f;
-        }
+        for (int y = 0; y < 4; ++y) m2 = __vmaxu2(m2, vw[y] & 0x7fff7fffu);
+        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = scale_exp(m);
+        if (m >= 0x7f80u) {
+          // infinities or NaN: the scale is of the finite ones.  In a draft's
+          // value they must not reach the rows that do not see it (0 x inf):
+          // the merge adds them where they are seen.
+          const bool hide = me.side && first + r >= len;
+          m = 0;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t lo = vw[y] & 0x7fffu, hi = (vw[y] >> 16) & 0x7fffu;
+            if (lo < 0x7f80u) m = max(m, lo);
+            else if (hide) vw[y] &= 0xffff0000u;
+            if (hi < 0x7f80u) m = max(m, hi);
+            else if (hide) vw[y] &= 0xffffu;
+          }
+          const uint32_t half = 0xffffu << (16 * hw);
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(half, m, o));
+          if (hide && c == 0) atomicOr(&a.inf_v[(int64_t)b * a.H + h], 1ull << (first + r - len));
+        }
+        const int e = scale_exp(m << 16);
         const float inv = exp_to_inv(e);
-        *reinterpret_cast<uint4*>(tile + swz(r, c)) =
-            make_uint4(pack_half2(x[0] * inv, x[1] * inv), pack_half2(x[2] * inv, x[3] * inv),
-                       pack_half2(x[4] * inv, x[5] * inv), pack_half2(x[6] * inv, x[7] * inv));
-        if (odd && me.side && t >= len) atomicOr(&a.inf_v[(int64_t)b * a.H + h], 1ull << (t - len));
-        if (c == 0) scales_of(sm, me.side, tl)[r] = m ? exp_to_f(e) : (me.side ? 0.f : 1.f);
+        uint32_t out[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          out[y] = pack_half2(__uint_as_float(vw[y] << 16) * inv, __uint_as_float(vw[y] & 0xffff0000u) * inv);
+        *reinterpret_cast<uint4*>(tile + swz(me.q * 32 + r, c)) = make_uint4(out[0], out[1], out[2], out[3]);
+        if (c == 0) scales[r] = m ? exp_to_f(e) : (me.side ? 0.f : 1.f);
       }
     }
     tc::fence_proxy_async_smem();
@@ -732,6 +771,14 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     tc::fence_barrier_init();
   }
   if (tid == 32) sm.rep = first_with_layout(a, b);
+  if (tail && warp == 2) {                            // the masks' columns
+    const unsigned long long lo = lane < n_new ? tree_mask(a, b, lane) : 0ull;
+    const unsigned long long hi = lane + 32 < n_new ? tree_mask(a, b, lane + 32) : 0ull;
+    for (int d = 0; d < n_new; ++d) {
+      const uint32_t x = __ballot_sync(0xffffffffu, (lo >> d) & 1ull), y = __ballot_sync(0xffffffffu, (hi >> d) & 1ull);
+      if (lane == 0) sm.seen[d] = make_uint2(x, y);
+    }
+  }
   if (tid < kOCols) {
     const int r = blk * NC + tid;
     sm.colt[tid] = (unsigned char)min(r / a.G, a.T - 1);
@@ -740,7 +787,6 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       sm.mp[i][tid] = -INFINITY;
       sm.cw[i][tid] = 1.f;
     }
-    if (tid < a.T) sm.mask[tid] = tree_mask(a, b, tid);
   }
   if (tid >= 128 && tid < 144) {
     const auto lev = [&](int c) { return c == 0 ? a.lev[0] : c == 1 ? a.lev[1] : c == 2 ? a.lev[2] : a.lev[3]; };
@@ -851,8 +897,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         special = (tile0 + i + 1) * kTT > len;
         live = t < len + n_new;
         if (special && live && t >= len) {
-          vis = 0;
-          for (int d = 0; d < a.T; ++d) vis |= ((sm.mask[d] >> (t - len)) & 1ull) << d;
+          const uint2 s = sm.seen[t - len];
+          vis = (unsigned long long)s.y << 32 | s.x;
         }
       } else {
         special = (tile0 + i + 1) * kTT > a.N;
@@ -1129,7 +1175,7 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
   int st = ANCHORKV_OK;
-  if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 1) / 2, 2 * a.H, a.batch), 256, 0, s, a);
+  if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 3) / 4, 2 * a.H, a.batch), 256, 0, s, a);
   if (st) return st;
   st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, smem_bytes<NC>(), s, a);
   if (st) return st;
