@@ -281,12 +281,30 @@ class PageSpec:
         return _TORCH_DT[self.dtype]
 
     @property
-    def pool_shape(self) -> tuple:
-        return (self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
+    def pool_shape(self) -> torch.Size:
+        return torch.Size((self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim))
 
     @property
     def state_numel(self) -> int:
         return 16 + 2 * self.n_pages + self.n_slots * (1 + self.max_pages)
+
+
+def _call(device, fn, *args) -> int:
+    """fn(*args, stream) with `device` current, on its current stream.  The
+    raw stream handle is a fraction of the cost of a Stream object, and the
+    smallest calls are bound by the host."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+
+
+def _require(name, t, shape, dtype, device):
+    """As _check_tensor, on one device."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _check_tensor(name, t, shape, dtype)
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def pages_state_bytes(pages: PageSpec) -> int:
@@ -304,20 +322,12 @@ def pages_workspace_bytes(pages: PageSpec) -> int:
     return n.value
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-
-
 def pages_init(pages: PageSpec, device="cuda", state: torch.Tensor | None = None) -> torch.Tensor:
     """A page state (int32) in which every page is free and every slot empty."""
     if state is None:
         state = torch.empty(pages_state_bytes(pages) // 4, dtype=torch.int32, device=device)
     _check_tensor("state", state, (pages.state_numel,), torch.int32)
-    with torch.cuda.device(state.device):
-        st = capi.lib().anchorkv_pages_init(ctypes.byref(pages.c()), _ptr(state), _stream(state.device))
-    capi.check("anchorkv_pages_init", st)
+    capi.check("anchorkv_pages_init", _call(state.device, capi.lib().anchorkv_pages_init, pages.c(), state.data_ptr()))
     return state
 
 
@@ -328,17 +338,23 @@ def pages_view(pages: PageSpec, state: torch.Tensor) -> dict:
             "len": state[at + 2 * n:at + 2 * n + s], "table": state[at + 2 * n + s:].view(s, pages.max_pages)}
 
 
-def _pages_check(pages, state, K_pages, V_pages, state_out, workspace):
-    _check_tensor("state", state, (pages.state_numel,), torch.int32)
-    _check_tensor("K_pages", K_pages, pages.pool_shape, pages.torch_dtype)
-    _check_tensor("V_pages", V_pages, pages.pool_shape, pages.torch_dtype)
+def _pages_args(pages, state, K_pages, V_pages, state_out, workspace):
+    """Checked state, pools and scratch: (C sizes, state_out, workspace, device)."""
+    dev, n, shape, dt = state.device, torch.Size((pages.state_numel,)), pages.pool_shape, pages.torch_dtype
+    if dev.type != "cuda":
+        raise ValueError("state must be a CUDA tensor")
+    _require("state", state, n, torch.int32, dev)
+    _require("K_pages", K_pages, shape, dt, dev)
+    _require("V_pages", V_pages, shape, dt, dev)
     if state_out is None:
         state_out = state
-    _check_tensor("state_out", state_out, (pages.state_numel,), torch.int32)
+    elif state_out is not state:
+        _require("state_out", state_out, n, torch.int32, dev)
     if workspace is None:
-        workspace = torch.empty(pages_workspace_bytes(pages), dtype=torch.uint8, device=state.device)
-    _same_device(state.device, K_pages=K_pages, V_pages=V_pages, state_out=state_out, workspace=workspace)
-    return state_out, workspace
+        workspace = torch.empty(pages_workspace_bytes(pages), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return pages.c(), state_out, workspace, dev
 
 
 def pages_commit(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
@@ -349,22 +365,20 @@ def pages_commit(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_
     n_accept: int32 [batch]; path: int32 [batch, n_draft].  Updates the state
     in place unless state_out is given; returns the new state.  Whether the
     operation was possible is in the state's status word (read_status)."""
-    state_out, workspace = _pages_check(pages, state, K_pages, V_pages, state_out, workspace)
+    pg, state_out, workspace, dev = _pages_args(pages, state, K_pages, V_pages, state_out, workspace)
     if K_new.dim() != 5:
         raise ValueError(f"K_new: expected [n_layers, batch, n_draft, H, D], got {tuple(K_new.shape)}")
     batch, drafts = K_new.shape[1:3]
-    shape = (pages.n_layers, batch, drafts, pages.n_kv_heads, pages.head_dim)
-    _check_tensor("K_new", K_new, shape, pages.torch_dtype)
-    _check_tensor("V_new", V_new, shape, pages.torch_dtype)
-    _check_tensor("n_accept", n_accept, (batch,), torch.int32)
+    shape = torch.Size((pages.n_layers, batch, drafts, pages.n_kv_heads, pages.head_dim))
+    _require("K_new", K_new, shape, pages.torch_dtype, dev)
+    _require("V_new", V_new, shape, pages.torch_dtype, dev)
+    _require("n_accept", n_accept, torch.Size((batch,)), torch.int32, dev)
     if path is not None:
-        _check_tensor("path", path, (batch, drafts), torch.int32)
-    _same_device(state.device, K_new=K_new, V_new=V_new, n_accept=n_accept, path=path)
-    with torch.cuda.device(state.device):
-        st = capi.lib().anchorkv_pages_commit(ctypes.byref(pages.c()), _ptr(state), _ptr(state_out), _ptr(K_pages),
-                                              _ptr(V_pages), _ptr(K_new), _ptr(V_new), batch, drafts, _ptr(path),
-                                              _ptr(n_accept), _ptr(workspace), workspace.numel(),
-                                              _stream(state.device))
+        _require("path", path, torch.Size((batch, drafts)), torch.int32, dev)
+    st = _call(dev, capi.lib().anchorkv_pages_commit, pg, state.data_ptr(), state_out.data_ptr(), K_pages.data_ptr(),
+               V_pages.data_ptr(), K_new.data_ptr(), V_new.data_ptr(), batch, drafts,
+               path.data_ptr() if path is not None else None, n_accept.data_ptr(), workspace.data_ptr(),
+               workspace.nbytes)
     capi.check("anchorkv_pages_commit", st)
     return state_out
 
@@ -375,13 +389,10 @@ def pages_fork(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_pa
     """Slot s becomes a copy of what slot parents[s] (int32 [n_slots]) was; -1
     empties it.  Full pages are shared, a partly filled last page is copied
     for all copies but the first.  Returns the new state."""
-    state_out, workspace = _pages_check(pages, state, K_pages, V_pages, state_out, workspace)
-    _check_tensor("parents", parents, (pages.n_slots,), torch.int32)
-    _same_device(state.device, parents=parents)
-    with torch.cuda.device(state.device):
-        st = capi.lib().anchorkv_pages_fork(ctypes.byref(pages.c()), _ptr(state), _ptr(state_out), _ptr(K_pages),
-                                            _ptr(V_pages), _ptr(parents), _ptr(workspace), workspace.numel(),
-                                            _stream(state.device))
+    pg, state_out, workspace, dev = _pages_args(pages, state, K_pages, V_pages, state_out, workspace)
+    _require("parents", parents, torch.Size((pages.n_slots,)), torch.int32, dev)
+    st = _call(dev, capi.lib().anchorkv_pages_fork, pg, state.data_ptr(), state_out.data_ptr(), K_pages.data_ptr(),
+               V_pages.data_ptr(), parents.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     capi.check("anchorkv_pages_fork", st)
     return state_out
 
@@ -389,11 +400,9 @@ def pages_fork(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_pa
 def pages_compact(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
                   state_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Move the pages in use to the front of the pool.  Returns the new state."""
-    state_out, workspace = _pages_check(pages, state, K_pages, V_pages, state_out, workspace)
-    with torch.cuda.device(state.device):
-        st = capi.lib().anchorkv_pages_compact(ctypes.byref(pages.c()), _ptr(state), _ptr(state_out), _ptr(K_pages),
-                                               _ptr(V_pages), _ptr(workspace), workspace.numel(),
-                                               _stream(state.device))
+    pg, state_out, workspace, dev = _pages_args(pages, state, K_pages, V_pages, state_out, workspace)
+    st = _call(dev, capi.lib().anchorkv_pages_compact, pg, state.data_ptr(), state_out.data_ptr(), K_pages.data_ptr(),
+               V_pages.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     capi.check("anchorkv_pages_compact", st)
     return state_out
 
@@ -406,18 +415,18 @@ def tree_workspace_bytes(p: AnchorKVParams, batch: int, drafts: int, pages: Page
     return n.value
 
 
-def _row_strides(name, t, shape, dtype):
+def _row_strides(name, t, shape, dtype, device):
     """(sequence, token) strides of a [batch, T, heads, D] tensor whose heads
     are contiguous; a dimension of one element has no stride to speak of."""
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     batch, drafts, heads, D = shape
-    if t.stride(3) != 1 or (heads > 1 and t.stride(2) != D):
+    seq, tok, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: heads must be contiguous, got strides {t.stride()}")
-    tok = t.stride(1) if drafts > 1 else heads * D
-    return t.stride(0) if batch > 1 else drafts * tok, tok
+    if drafts == 1:
+        tok = heads * D
+    return seq if batch > 1 else drafts * tok, tok
 
 
 def tree_attn(p: AnchorKVParams, compressed: torch.Tensor | None, q: torch.Tensor, K_new: torch.Tensor,
@@ -440,50 +449,54 @@ def tree_attn(p: AnchorKVParams, compressed: torch.Tensor | None, q: torch.Tenso
         raise ValueError(f"q: expected [batch, n_draft, H_q, D], got {tuple(q.shape)}")
     batch, drafts = q.shape[:2]
     H, Hq, D, dt, dev = p.n_kv_heads, p.n_q_heads, p.head_dim, p.torch_dtype, q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    L, pc = capi.lib(), p.c()
+    shape, kv_shape, b_shape = torch.Size((batch, drafts, Hq, D)), torch.Size((batch, drafts, H, D)), torch.Size((batch,))
     t = capi.Tree(batch=batch, n_draft=drafts)
-    t.q_seq_stride, t.q_tok_stride = _row_strides("q", q, (batch, drafts, Hq, D), dt)
-    t.new_seq_stride, t.new_tok_stride = _row_strides("K_new", K_new, (batch, drafts, H, D), dt)
-    if _row_strides("V_new", V_new, (batch, drafts, H, D), dt) != (t.new_seq_stride, t.new_tok_stride):
+    t.q_seq_stride, t.q_tok_stride = _row_strides("q", q, shape, dt, dev)
+    t.new_seq_stride, t.new_tok_stride = strides = _row_strides("K_new", K_new, kv_shape, dt, dev)
+    if _row_strides("V_new", V_new, kv_shape, dt, dev) != strides:
         raise ValueError(f"K_new and V_new: unequal strides {K_new.stride()} and {V_new.stride()}")
     if compressed is not None:
-        if compressed.device.type != "cuda" or compressed.dtype != torch.uint8 or not compressed.is_contiguous():
-            raise ValueError("compressed must be a contiguous CUDA uint8 tensor")
-        if compressed.dim() == 1:
-            t.n_layouts, t.seq_stride_bytes = 1, (compressed.numel() + 15) // 16 * 16
-        else:
-            t.n_layouts, t.seq_stride_bytes = compressed.shape
-        if compressed.shape[-1] < anchorkv_bytes(p)["total_bytes"]:
-            raise ValueError(f"compressed: {compressed.shape[-1]} bytes are less than a layout")
+        if compressed.device != dev or compressed.dtype != torch.uint8 or not compressed.is_contiguous():
+            raise ValueError(f"compressed must be a contiguous uint8 tensor on {dev}")
+        size = compressed.shape[-1]
+        lay = capi.Layout()
+        capi.check("anchorkv_bytes", L.anchorkv_bytes(pc, lay))
+        if size < lay.total_bytes:
+            raise ValueError(f"compressed: {size} bytes are less than a layout ({lay.total_bytes})")
+        t.n_layouts, t.seq_stride_bytes = (1, (size + 15) // 16 * 16) if compressed.dim() == 1 else compressed.shape
         t.compressed = compressed.data_ptr()
     if layout_of is not None:
-        _check_tensor("layout_of", layout_of, (batch,), torch.int32)
+        _require("layout_of", layout_of, b_shape, torch.int32, dev)
         t.layout_of = layout_of.data_ptr()
     if n_new is not None:
-        _check_tensor("n_new", n_new, (batch,), torch.int32)
+        _require("n_new", n_new, b_shape, torch.int32, dev)
         t.n_new = n_new.data_ptr()
     if mask is not None:
-        _check_tensor("mask", mask, (batch, drafts), torch.int64)
+        _require("mask", mask, shape[:2], torch.int64, dev)
         t.mask = mask.data_ptr()
     if pages is not None:
         if state is None or K_pages is None or V_pages is None:
             raise ValueError("pages need state, K_pages and V_pages")
-        _check_tensor("state", state, (pages.state_numel,), torch.int32)
-        _check_tensor("K_pages", K_pages, pages.pool_shape[1:], dt)
-        _check_tensor("V_pages", V_pages, pages.pool_shape[1:], dt)
+        pool = pages.pool_shape[1:]
+        _require("state", state, torch.Size((pages.state_numel,)), torch.int32, dev)
+        _require("K_pages", K_pages, pool, dt, dev)
+        _require("V_pages", V_pages, pool, dt, dev)
         pg = pages.c()
         t.pages = ctypes.pointer(pg)
         t.state, t.K_pages, t.V_pages = state.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr()
     if out is None:
-        out = torch.zeros(batch, drafts, Hq, D, dtype=dt, device=dev)
-    _check_tensor("out", out, (batch, drafts, Hq, D), dt)
+        out = torch.zeros(shape, dtype=dt, device=dev)
+    else:
+        _require("out", out, shape, dt, dev)
     if workspace is None:
         workspace = torch.empty(tree_workspace_bytes(p, batch, drafts, pages), dtype=torch.uint8, device=dev)
-    _same_device(dev, compressed=compressed, K_new=K_new, V_new=V_new, n_new=n_new, mask=mask, layout_of=layout_of,
-                 state=state, K_pages=K_pages, V_pages=V_pages, out=out, workspace=workspace)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
     t.q, t.K_new, t.V_new, t.out = q.data_ptr(), K_new.data_ptr(), V_new.data_ptr(), out.data_ptr()
-    with torch.cuda.device(dev):
-        st = capi.lib().anchorkv_tree_attn(ctypes.byref(p.c()), ctypes.byref(t), _ptr(workspace), workspace.numel(),
-                                           _stream(dev))
+    st = _call(dev, L.anchorkv_tree_attn, pc, t, workspace.data_ptr(), workspace.nbytes)
     capi.check("anchorkv_tree_attn", st)
     return out
 

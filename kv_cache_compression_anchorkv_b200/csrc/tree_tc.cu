@@ -1195,19 +1195,32 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
   // shortest.
   constexpr int64_t kFixed = 6;
   constexpr int kRows[4] = {16, 32, 64, 128}, kTime[4] = {12, 14, 17, 29};
-  const int64_t pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (tp->cap + tp->T + kTT - 1) / kTT;
+  const int pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (int)((tp->cap + tp->T + kTT - 1) / kTT);
   int64_t best = INT64_MAX;
   for (int k = 0; k < 4; ++k) {
-    const int64_t n_blk = (tp->rows + kRows[k] - 1) / kRows[k], units = (int64_t)tp->batch * pl.H * n_blk;
-    for (int64_t s = prefix ? 1 : 0; s <= std::min<int64_t>(pre, 148); ++s) {
-      const int64_t per = s ? (pre + s - 1) / s : 8, t = (tail + std::max<int64_t>(per, 4) - 1) / std::max<int64_t>(per, 4);
-      const int64_t waves = (units * (s + t) + 147) / 148, cost = waves * (per + kFixed) * kTime[k];
+    const int n_blk = (tp->rows + kRows[k] - 1) / kRows[k], units = tp->batch * pl.H * n_blk;
+    // as many CTAs a unit as fill a whole number of waves
+    const int first = std::max(1, (units * (prefix ? 2 : 1) + 147) / 148);
+    for (int waves = first; waves < first + 16; ++waves) {
+      const int ctas = 148 * waves / units;
+      int s = 0, per = 8, t = 1;
+      if (prefix) {
+        s = std::min(pre, std::max(1, ctas - 1));
+        per = (pre + s - 1) / s;
+        t = (tail + std::max(per, 4) - 1) / std::max(per, 4);
+        s = std::min(pre, std::max(1, ctas - t));
+        per = (pre + s - 1) / s;
+      } else {
+        t = std::min(tail, std::max(1, ctas));
+        per = (tail + t - 1) / t;
+      }
+      const int64_t cost = ((int64_t)units * (s + t) + 147) / 148 * (std::max(per, (tail + t - 1) / t) + kFixed) * kTime[k];
       if (cost < best) {
         best = cost;
         tp->RB = kRows[k];
-        tp->n_blk = (int)n_blk;
-        tp->parts = (int)(s + t);
-        tp->tail_parts = (int)t;
+        tp->n_blk = n_blk;
+        tp->parts = s + t;
+        tp->tail_parts = t;
       }
     }
   }
