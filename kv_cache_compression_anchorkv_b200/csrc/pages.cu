@@ -202,28 +202,36 @@ __global__ void __launch_bounds__(kMetaThreads) commit_state_kernel(PgArgs a) {
 }
 
 // One warp per (layer, side, sequence, accepted row): the row of all heads is
-// contiguous in the drafts and H pieces of D elements in the page.
+// contiguous in the drafts and H pieces of D elements in the page.  What the
+// rows of a sequence share is fetched ahead of the row's own lookups, and a
+// lane's pieces are in flight together.
 __global__ void __launch_bounds__(256) commit_rows_kernel(PgArgs a) {
-  wait_for_primary();
-  if (a.ws[0] == 0) return;
   const int lane = threadIdx.x & 31;
   const int64_t n_rows = (int64_t)a.batch * a.T, units = n_rows * 2 * a.L;
   const int64_t warps = (int64_t)gridDim.x * 8;
-  const int pieces = a.H * a.row16;
+  const int pieces = a.H * a.row16, shift = a.row16 == 16 ? 4 : 5, page16 = a.P * a.row16;
+  wait_for_primary();
+  if (a.ws[0] == 0) return;
   for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += warps) {
     const int64_t ls = u / n_rows, r = u % n_rows;
     const int b = (int)(r / a.T), i = (int)(r % a.T), side = (int)(ls & 1);
     const int64_t l = ls >> 1;
-    const int n = a.n_accept[b];
+    const int n = a.n_accept[b], len = a.out[o_len(a) + b], src = a.path ? a.path[(int64_t)b * a.T + i] : i;
     if (i >= n) continue;
-    const int pos = a.out[o_len(a) + b] - n + i;
+    const int pos = len - n + i;
     const int pg = a.out[o_table(a) + (int64_t)b * a.maxp + pos / a.P];
-    const int src = a.path ? a.path[(int64_t)b * a.T + i] : i;
     const uint4* from = a.fresh[side] + ((l * a.batch + b) * a.T + src) * pieces;
-    uint4* to = a.pool[side] + (l * a.n_pages + pg) * a.H * a.P * a.row16 + (int64_t)(pos % a.P) * a.row16;
-    for (int x = lane; x < pieces; x += 32) {
-      const int h = x / a.row16, c = x % a.row16;
-      to[(int64_t)h * a.P * a.row16 + c] = from[x];
+    uint4* to = a.pool[side] + (l * a.n_pages + pg) * a.H * page16 + (int64_t)(pos % a.P) * a.row16;
+    for (int x0 = lane; x0 < pieces; x0 += 32 * 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (x0 + 32 * k < pieces) v[k] = from[x0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = x0 + 32 * k;
+        if (x < pieces) to[(int64_t)(x >> shift) * page16 + (x & (a.row16 - 1))] = v[k];
+      }
     }
   }
 }
@@ -441,24 +449,43 @@ __global__ void __launch_bounds__(kMetaThreads) compact_state_kernel(PgArgs a) {
   header_out(a, status, a.n_pages - n, moves);
 }
 
-// Moves the listed pages' rows: one CTA per (page, layer, side, head), whose
-// rows are contiguous.  Sources and destinations of a list never overlap.
+// Moves the listed pages' rows: a CTA takes 32 KB of a (page, layer, side) at a
+// time (H runs of contiguous rows), eight 16-byte pieces a thread in flight.
+// Sources and destinations of a list never overlap.
+constexpr int kChunk = 256 * 8;
+
 __global__ void __launch_bounds__(256) copy_pages_kernel(PgArgs a) {
   wait_for_primary();
   const int items = a.ws[0];
   const int* list = a.ws + w_list(a);
   const int64_t most = list_most(a.n_pages, a.S);
-  const int per = 2 * a.L * a.H;
-  const int64_t units = (int64_t)items * per, page16 = (int64_t)a.P * a.row16;
+  const int page16 = a.P * a.row16, chunks = (a.H * page16 + kChunk - 1) / kChunk, per = 2 * a.L * chunks;
+  const int64_t units = (int64_t)items * per;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int i = (int)(u / per), x = (int)(u % per);
-    const int h = x % a.H, side = (x / a.H) & 1;
-    const int64_t l = x / (2 * a.H), base = l * a.n_pages;
-    const uint4* from = a.pool[side] + ((base + list[i]) * a.H + h) * page16;
-    uint4* to = a.pool[side] + ((base + list[most + i]) * a.H + h) * page16;
-    const int n = list[2 * most + i] * a.row16;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < n; c += 256) to[c] = from[c];
+    const int i = (int)(u / per), x = (int)(u % per), ls = x / chunks;
+    const int n = list[2 * most + i] * a.row16, total = n * a.H;      // pieces of a head, of all
+    const int c0 = (x % chunks) * kChunk + threadIdx.x;
+    if (c0 >= total) continue;
+    const int64_t base = (int64_t)(ls >> 1) * a.n_pages;
+    const uint4* from = a.pool[ls & 1] + (base + list[i]) * a.H * page16;
+    uint4* to = a.pool[ls & 1] + (base + list[most + i]) * a.H * page16;
+    // piece c is at c, or, of a page that is not full, head by head
+    int at[8], h = 0, r = c0;
+    if (n < page16) { h = c0 / n; r = c0 % n; }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      at[k] = h * page16 + r;
+      r += 256;
+      if (n < page16)
+        while (r >= n) { r -= n; ++h; }
+    }
+    uint4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c0 + 256 * k < total) v[k] = from[at[k]];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c0 + 256 * k < total) to[at[k]] = v[k];
   }
 }
 
@@ -477,6 +504,8 @@ int make_args(const anchorkv_pages* pg, PgArgs* a) {
   a->row16 = kD * (pg->dtype == ANCHORKV_BF16 ? 2 : 4) / 16;
   return ANCHORKV_OK;
 }
+
+int64_t copy_chunks(const PgArgs& a) { return ((int64_t)a.H * a.P * a.row16 + kChunk - 1) / kChunk; }
 
 int64_t ws_ints(const PgArgs& a) { return w_table(a) + (int64_t)a.S * a.maxp; }
 
@@ -598,7 +627,7 @@ int anchorkv_pages_fork(const anchorkv_pages* pg, const int32_t* state_in, int32
   stage_begin(kStPages, s);
   fork_state_kernel<<<1, kMetaThreads, smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  st = launch_rows(copy_pages_kernel, std::min<int64_t>((int64_t)a.S * 2 * a.L * a.H, kRowGrid), a, s);
+  st = launch_rows(copy_pages_kernel, std::min<int64_t>((int64_t)a.S * 2 * a.L * copy_chunks(a), kRowGrid), a, s);
   stage_end(kStPages, s, 2);
   return st;
 }
@@ -612,7 +641,7 @@ int anchorkv_pages_compact(const anchorkv_pages* pg, const int32_t* state_in, in
   stage_begin(kStPages, s);
   compact_state_kernel<<<1, kMetaThreads, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  st = launch_rows(copy_pages_kernel, std::min<int64_t>((int64_t)(a.n_pages / 2 + 1) * 2 * a.L * a.H, kRowGrid), a, s);
+  st = launch_rows(copy_pages_kernel, std::min<int64_t>((int64_t)(a.n_pages / 2 + 1) * 2 * a.L * copy_chunks(a), kRowGrid), a, s);
   stage_end(kStPages, s, 2);
   return st;
 }

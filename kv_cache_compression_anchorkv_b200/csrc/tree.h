@@ -8,6 +8,9 @@ namespace akv {
 
 // Drafts of one sequence: bits of a mask word.
 constexpr int kTreeMaxDrafts = 64;
+// Reference (a NaN) of a part whose sequence could not be read; its sum is NaN
+// too, and the merge latches the error.
+constexpr uint32_t kTreeBadPart = 0x7fc0bad0u;
 
 // One call's shape: the rows (draft t, query head g) of a KV head, r = t G + g,
 // are cut into blocks of RB; every (sequence, head, block) is a unit, whose

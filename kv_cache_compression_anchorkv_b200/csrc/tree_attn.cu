@@ -128,7 +128,7 @@ int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* w
   a.anc = w + tp.o_anc;
   a.anc_scale = (float*)(w + tp.o_anc_scale);
   a.meta = w + tp.o_meta;
-  a.inf_v = (unsigned long long*)(w + tp.o_inf);
+  a.inf_v = p->dtype == ANCHORKV_BF16 ? (unsigned long long*)(w + tp.o_inf) : nullptr;
   stage_begin(kStTree, s);
   st = p->dtype == ANCHORKV_BF16 ? launch_tree_tc(a, s) : launch_tree_simt(a, s);
   stage_end(kStTree, s, p->dtype != ANCHORKV_BF16 ? 2 : t->compressed ? 4 : 3);
