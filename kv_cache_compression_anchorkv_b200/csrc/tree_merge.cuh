@@ -23,7 +23,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&c)[4]) {
 // latency of the parts' reads from L2, so they are spread over warps.
 template <typename T>
 __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int rb) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float4 sum[2][4][2][32];
   __shared__ float2 lm[2][4];
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, grp = threadIdx.x >> 7;
@@ -31,28 +30,42 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int rb) {
   const int Hq = a.H * a.G;
   const bool there = i < (int64_t)a.batch * a.T * Hq;
   const int b = there ? (int)(i / (a.T * Hq)) : 0, t = (int)(i / Hq % a.T), hq = (int)(i % Hq), h = hq / a.G;
-  if (!there || t >= tree_new(a, b)) return;
+  const bool wanted = there && t < tree_new(a, b);
+  const unsigned long long seen = wanted && a.inf_v ? tree_mask(a, b, t) : 0ull;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!wanted) return;
   const int r = t * a.G + hq % a.G;
   const int64_t unit = ((int64_t)b * a.H + h) * a.n_blk + r / rb;
   const float2* ml = reinterpret_cast<const float2*>(a.ml) + unit * a.parts * rb + r % rb;
   const float* o = a.part + (unit * a.parts * rb + r % rb) * kD + lane * 4;
+  unsigned long long odd = wq == 0 && seen ? a.inf_v[(int64_t)b * a.H + h] & seen : 0ull;
   // parts wq, wq + 4, ...: exact tokens' (y) and compressed tokens' (x) in units
-  // of the largest reference met so far
+  // of the largest reference met so far; four parts' loads in flight
   float m = -INFINITY, l = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-#pragma unroll 4
-  for (int s = wq; s < a.parts; s += 4) {
-    const float2 e = ml[(int64_t)s * rb];
-    const float4 v = *reinterpret_cast<const float4*>(o + (int64_t)s * rb * kD);
-    if (__float_as_uint(e.x) == kTreeBadPart && lane == 0) latch_error(a.counters, kDevErrBounds);
-    if (e.y == 0.f) continue;
-    const float mn = fmaxf(m, e.x), f = m > -INFINITY ? exp2f(m - mn) : 0.f, g = exp2f(e.x - mn);
-    m = mn;
-    l = l * f + e.y * g;
-    x.x *= f; x.y *= f; x.z *= f; x.w *= f;
-    y.x *= f; y.y *= f; y.z *= f; y.w *= f;
-    float4& z = s < a.tail_parts ? y : x;
-    z.x = fmaf(v.x, g, z.x); z.y = fmaf(v.y, g, z.y); z.z = fmaf(v.z, g, z.z); z.w = fmaf(v.w, g, z.w);
+  for (int s0 = wq; s0 < a.parts; s0 += 16) {
+    float2 e[4];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int s = min(s0 + 4 * k, a.parts - 1);
+      e[k] = ml[(int64_t)s * rb];
+      v[k] = *reinterpret_cast<const float4*>(o + (int64_t)s * rb * kD);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int s = s0 + 4 * k;
+      if (s >= a.parts) break;
+      if (__float_as_uint(e[k].x) == kTreeBadPart && lane == 0) latch_error(a.counters, kDevErrBounds);
+      if (e[k].y == 0.f) continue;
+      const float mn = fmaxf(m, e[k].x), f = m > -INFINITY ? exp2f(m - mn) : 0.f, g = exp2f(e[k].x - mn);
+      m = mn;
+      l = l * f + e[k].y * g;
+      x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+      y.x *= f; y.y *= f; y.z *= f; y.w *= f;
+      float4& z = s < a.tail_parts ? y : x;
+      z.x = fmaf(v[k].x, g, z.x); z.y = fmaf(v[k].y, g, z.y); z.z = fmaf(v[k].z, g, z.z); z.w = fmaf(v[k].w, g, z.w);
+    }
   }
   sum[grp][wq][0][lane] = x;
   sum[grp][wq][1][lane] = y;
@@ -85,7 +98,6 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int rb) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] = (c[e] + d[e]) * inv;
   // infinities and NaN of the drafts' values, for the rows that see them
-  unsigned long long odd = a.inf_v ? a.inf_v[(int64_t)b * a.H + h] & tree_mask(a, b, t) : 0ull;
   while (odd) {
     const int k = __ffsll((long long)odd) - 1;
     odd &= odd - 1;

@@ -271,25 +271,32 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
       reinterpret_cast<const __nv_bfloat16*>(a.comp + (int64_t)lay * a.stride + (side ? a.off_av : a.off_ak)) +
       (int64_t)h * a.k * kD;
   const int64_t row0 = ((int64_t)b * 2 * a.H + sh) * a.k;
-  for (int s = blockIdx.x * 8 + warp; s < a.k; s += gridDim.x * 8) {
-    float v[4];
-    load4<__nv_bfloat16>(src + (int64_t)s * kD + lane * 4, v);
-    if (!a.naive) {
+  for (int s = (blockIdx.x * 8 + warp) * 2; s < a.k; s += gridDim.x * 16) {
+    const int s1 = min(s + 1, a.k - 1);                  // two rows' latencies together
+    float v[2][4];
+    load4<__nv_bfloat16>(src + (int64_t)s * kD + lane * 4, v[0]);
+    load4<__nv_bfloat16>(src + (int64_t)s1 * kD + lane * 4, v[1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = 4 * lane + i;
-        if ((a.sign_bits[d >> 5] >> (d & 31)) & 1u) v[i] = -v[i];
+    for (int k = 0; k < 2; ++k) {
+      if (!a.naive) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = 4 * lane + i;
+          if ((a.sign_bits[d >> 5] >> (d & 31)) & 1u) v[k][i] = -v[k][i];
+        }
+        fwht128(v[k]);
       }
-      fwht128(v);
+      const float m = warp_max(fmaxf(fmaxf(fabsf(v[k][0]), fabsf(v[k][1])), fmaxf(fabsf(v[k][2]), fabsf(v[k][3]))));
+      const int e = scale_exp(__float_as_uint(m)), row = k ? s1 : s;
+      const float inv = exp_to_inv(e);
+      reinterpret_cast<uint2*>(a.anc)[(row0 + row) * 32 + lane] =
+          make_uint2(pack_half2(v[k][0] * inv, v[k][1] * inv), pack_half2(v[k][2] * inv, v[k][3] * inv));
+      if (lane == 0) a.anc_scale[row0 + row] = exp_to_f(e) * (a.naive ? 1.f : rsqrtf((float)kD));
     }
-    const float m = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-    const int e = scale_exp(__float_as_uint(m));
-    const float inv = exp_to_inv(e);
-    reinterpret_cast<uint2*>(a.anc)[(row0 + s) * 32 + lane] =
-        make_uint2(pack_half2(v[0] * inv, v[1] * inv), pack_half2(v[2] * inv, v[3] * inv));
-    if (lane == 0) a.anc_scale[row0 + s] = exp_to_f(e) * (a.naive ? 1.f : rsqrtf((float)kD));
   }
 }
+
+constexpr int kMetaTiles = 4;
 
 // Token tables of every layout in use, one warp per 32 tokens of a side and
 // head, after the anchors' scales: what a token row is multiplied by,
@@ -298,11 +305,13 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
 // (2 KB a tile and side).
 __global__ void __launch_bounds__(256) tree_meta_kernel(TreeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kTiles = 2;                              // a warp's tiles, their loads in flight together
+  constexpr int kTiles = kMetaTiles;                     // a warp's tiles, their loads in flight together
   const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, b = blockIdx.z, sh = blockIdx.y;
-  if (first_with_layout(a, b) != b) return;
   const int lay = tree_layout(a, b);
-  if (lay < 0) return;
+  if (lay < 0 || first_with_layout(a, b) != b) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // this kernel is over after the one before it
+    return;
+  }
   const uint8_t* comp = a.comp + (int64_t)lay * a.stride;
   const uint32_t* words = reinterpret_cast<const uint32_t*>(comp + a.off_tok) + (int64_t)sh * a.N;
   const uint4* bms = reinterpret_cast<const uint4*>(comp + a.off_bm) + (int64_t)sh * a.n_tiles;
@@ -1075,11 +1084,11 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
       ready_dev = dev;
     }
   }
-  const int gx = a.comp ? std::max(1, std::min((a.k + 7) / 8, 256)) : 1;
+  const int gx = a.comp ? std::max(1, std::min((a.k + 15) / 16, 256)) : 1;
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
   int st = ANCHORKV_OK;
-  if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 3) / 4, 2 * a.H, a.batch), 256, 0, s, a);
+  if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 2 * kMetaTiles - 1) / (2 * kMetaTiles), 2 * a.H, a.batch), 256, 0, s, a);
   if (st) return st;
   st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, smem_bytes<NC>(), s, a);
   if (st) return st;
