@@ -450,8 +450,14 @@ int anchorkv_tree_workspace_bytes(const anchorkv_params* p, int32_t batch, int32
  * contiguous and heads are D apart.  The call overwrites `ws`, whose first
  * words are a status word and counters: a layout_of or page-table entry out of
  * its range latches code 3 there (anchorkv_read_device_status) and the rows of
- * that sequence become NaN.  EUNSUPPORTED when batch * H > 65535 or the page
- * tables reach more than 2^20 tokens.
+ * that sequence become NaN; code 4 is a bounded wait that timed out.  Calls
+ * that may overlap (two streams, two graphs) need a workspace each.
+ * EUNSUPPORTED when batch * H > 65535, H > 32767 or the page tables reach more
+ * than 2^20 tokens.
+ * bf16 caches: logits and values on the tensor cores with fp16 operands (rows
+ * over powers of two) and fp32 accumulators, sums and scales; the output is
+ * rounded once.  fp32 caches: fp32 throughout.  Output is bit-for-bit
+ * deterministic.
  */
 int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* ws, size_t ws_bytes, void* stream);
 

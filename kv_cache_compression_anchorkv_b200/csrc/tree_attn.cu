@@ -12,7 +12,7 @@ int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pa
   int st = make_plan(p, pl);
   if (st) return st;
   if (batch < 0 || T < 1 || T > kTreeMaxDrafts) return ANCHORKV_EINVAL;
-  if ((int64_t)batch * pl->H > 65535) return ANCHORKV_EUNSUPPORTED;      // grid z
+  if ((int64_t)batch * pl->H > 65535 || pl->H > 32767) return ANCHORKV_EUNSUPPORTED;      // grids: sequences x heads, sides x heads
   *tp = TreePlan{};
   tp->batch = std::max(batch, 1);
   tp->T = T;

@@ -2,16 +2,18 @@
 //
 // "AnchorKV: Anchor-Residual KV Cache Compression" (pith.science review),
 // Referee "Summary": a FlashAttention-style decoder rebuilds tiles when they
-// are consumed.  A block of 16 rows (draft, query head) of one (sequence, KV
-// head) walks its share of the tokens - compressed, paged, drafted, in this
-// order - in tiles of 32: one warp rebuilds a token,
+// are consumed.  A block of 16 or 64 rows (draft, query head) of one (sequence,
+// KV head) walks its share of the tokens - compressed, paged, drafted, in this
+// order - in tiles of 32: a warp rebuilds its four tokens' keys and values,
 //   x^_t = gamma_t x_a(t) + sigma_t s . H lev(c_t) / sqrt(D),
-// into shared memory, then 256 threads take the 16 x 32 logits, the running
-// maximum and sum of the softmax, and the 16 x 128 products with the values,
-// which stay in registers.  Everything is held in 32 bits: an fp32 cache is
-// answered in fp32 accuracy, which the tensor cores' operand types are short
-// of.  Bound by shared-memory reads of the products (a K element feeds four
-// multiplications, a V element eight).
+// into shared memory, then 256 threads take the logits, the running maximum and
+// sum of the softmax, and the products with the values, which stay in
+// registers.  Everything is held in 32 bits: an fp32 cache is answered in fp32
+// accuracy, which the tensor cores' operand types are short of.
+// Sixteen rows serve single tokens and small trees, where the latency of one
+// tile counts; 64 rows share a rebuilt tile and read shared memory six times
+// for 32 multiplications (logits) and three times (values), against three and
+// two for eight, and are bound by those multiplications.
 #include <algorithm>
 #include <mutex>
 
@@ -22,20 +24,19 @@
 namespace akv {
 namespace {
 
-constexpr int kRB = 16;        // rows of a block
 constexpr int kTT = 32;        // tokens of a tile
 constexpr int kThr = 256;
 constexpr int kKPitch = kD + 4;  // floats; a quarter-warp's float4 reads hit all banks
-constexpr int kPPitch = kRB + 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
+template <int RB>
 struct Sm {
-  float q[kRB][kD];
+  float q[RB][kD];
   float K[kTT][kKPitch];
   float V[kTT][kD];
-  float P[kTT][kPPitch];
-  float scale[kRB];
-  unsigned long long mask[kRB];
+  float P[kTT][RB + 4];
+  float scale[RB];
+  unsigned long long mask[RB];
 };
 
 // A warp's tokens of a tile, each as a key and a value: item i < 2 kOwn is
@@ -90,9 +91,11 @@ __device__ __forceinline__ Item find_item(const TreeArgs& a, const uint8_t* comp
   return it;
 }
 
-__global__ void __launch_bounds__(kThr) tree_simt_kernel(TreeArgs a) {
+template <int kRB>
+__global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
+  constexpr int kRW = kRB / 8;                        // rows of a warp in the softmax and the values' products
   extern __shared__ __align__(16) unsigned char raw[];
-  Sm& sm = *reinterpret_cast<Sm*>(raw);
+  Sm<kRB>& sm = *reinterpret_cast<Sm<kRB>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = blockIdx.x, blk = blockIdx.y, bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
   const int64_t unit = (int64_t)bh * a.n_blk + blk;
@@ -119,12 +122,15 @@ __global__ void __launch_bounds__(kThr) tree_simt_kernel(TreeArgs a) {
     const int r = blk * kRB + tid;
     sm.mask[tid] = r < rows ? tree_mask(a, b, r / a.G) : 0ull;
   }
-  float acc[8];
+  float acc[kRW][4];                                  // four columns of each row
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  // softmax state of rows 2 warp and 2 warp + 1, the same in every lane
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  const int d_o = tid & 127, half = tid >> 7;         // this thread's output column, rows 8 half .. + 7
+  for (int i = 0; i < kRW; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+  // softmax state of the warp's rows, the same in every lane
+  float m[kRW], l[kRW];
+#pragma unroll
+  for (int i = 0; i < kRW; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
   __shared__ int bad_page;
   if (tid == 0) bad_page = 0;
   __syncthreads();
@@ -180,76 +186,109 @@ __global__ void __launch_bounds__(kThr) tree_simt_kernel(TreeArgs a) {
       }
     }
     __syncthreads();
+    // logits: tokens j and (64 rows) j + 16, kSR rows
     {
-      // logits: token j, rows 2 g and 2 g + 1
-      const int j = tid & 31, g = tid >> 5;
-      float s[2] = {0.f, 0.f};
-#pragma unroll 8
-      for (int d = 0; d < kD; d += 4) {
-        const float4 kv = *reinterpret_cast<const float4*>(&sm.K[j][d]);
+      constexpr int kSR = kRB == 16 ? 2 : 4, kST = kRB == 16 ? 1 : 2;
+      const int j = kRB == 16 ? tid & 31 : tid & 15, g = kRB == 16 ? tid >> 5 : tid >> 4;
+      float s[kST][kSR];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 qv = *reinterpret_cast<const float4*>(&sm.q[2 * g + i][d]);
-          s[i] = fmaf(qv.x, kv.x, s[i]);
-          s[i] = fmaf(qv.y, kv.y, s[i]);
-          s[i] = fmaf(qv.z, kv.z, s[i]);
-          s[i] = fmaf(qv.w, kv.w, s[i]);
+      for (int t = 0; t < kST; ++t)
+#pragma unroll
+        for (int i = 0; i < kSR; ++i) s[t][i] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < kD; d += 4) {
+        float4 kv[kST];
+#pragma unroll
+        for (int t = 0; t < kST; ++t) kv[t] = *reinterpret_cast<const float4*>(&sm.K[j + 16 * t][d]);
+#pragma unroll
+        for (int i = 0; i < kSR; ++i) {
+          const float4 qv = *reinterpret_cast<const float4*>(&sm.q[kSR * g + i][d]);
+#pragma unroll
+          for (int t = 0; t < kST; ++t) {
+            s[t][i] = fmaf(qv.x, kv[t].x, s[t][i]);
+            s[t][i] = fmaf(qv.y, kv[t].y, s[t][i]);
+            s[t][i] = fmaf(qv.z, kv[t].z, s[t][i]);
+            s[t][i] = fmaf(qv.w, kv[t].w, s[t][i]);
+          }
         }
       }
-      // ... whose softmax is this warp's: lane = token
-      const int u = tt + j - n_pre - len;                  // draft index, negative before the drafts
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * warp + i;
-        const bool off = j >= nt || (u >= 0 && !((sm.mask[r] >> u) & 1ull));
-        // fmaxf passes NaN over; a NaN logit that is seen comes back through its
-        // exponential.  Masked places hold -1, so that the products leave them out
-        // whatever the value's row holds.
-        const float mn = fmaxf(m[i], warp_max(off ? -INFINITY : s[i]));
-        const float sc = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
-        const float p = off ? -1.f : (mn == -INFINITY && s[i] == mn) ? 0.f : exp2f(s[i] - mn);
-        l[i] = l[i] * sc + warp_sum(off ? 0.f : p);
-        m[i] = mn;
-        sm.P[j][r] = p;
-        if (lane == 0) sm.scale[r] = sc;
-      }
+      for (int t = 0; t < kST; ++t)
+#pragma unroll
+        for (int i = 0; i < kSR; ++i) sm.P[j + 16 * t][kSR * g + i] = s[t][i];
     }
     __syncthreads();
+    // softmax: lane = token.  Masked places of a tile with drafts become -1, so
+    // that the products leave them out whatever the value's row holds; tokens
+    // behind the last have zero rows.
+    const int u = tt + lane - n_pre - len;                 // draft index, negative before the drafts
+    const bool drafts = tt + nt > n_pre + len;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= sm.scale[8 * half + i];
+    for (int i = 0; i < kRW; ++i) {
+      const int r = kRW * warp + i;
+      const float s = sm.P[lane][r];
+      const bool off = lane >= nt || (u >= 0 && !((sm.mask[r] >> u) & 1ull));
+      // fmaxf passes NaN over; a NaN logit that is seen comes back through its exponential
+      const float mn = fmaxf(m[i], warp_max(off ? -INFINITY : s));
+      const float sc = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
+      const float p = off ? 0.f : (mn == -INFINITY && s == mn) ? 0.f : exp2f(s - mn);
+      l[i] = l[i] * sc + warp_sum(p);
+      m[i] = mn;
+      sm.P[lane][r] = off && drafts ? -1.f : p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] *= sc;
+    }
+    __syncwarp();                                          // the warp's own rows
+    if (drafts) {
+      for (int j = 0; j < nt; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.V[j][lane * 4]);
+#pragma unroll
+        for (int i = 0; i < kRW; ++i) {
+          const float p = sm.P[j][kRW * warp + i];
+          if (p < 0.f) continue;
+          acc[i][0] = fmaf(p, v.x, acc[i][0]);
+          acc[i][1] = fmaf(p, v.y, acc[i][1]);
+          acc[i][2] = fmaf(p, v.z, acc[i][2]);
+          acc[i][3] = fmaf(p, v.w, acc[i][3]);
+        }
+      }
+    } else {
 #pragma unroll 4
-    for (int j = 0; j < kTT; ++j) {
-      const float v = sm.V[j][d_o];
-      const float4 pa = *reinterpret_cast<const float4*>(&sm.P[j][8 * half]);
-      const float4 pb = *reinterpret_cast<const float4*>(&sm.P[j][8 * half + 4]);
-      const float p[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+      for (int j = 0; j < kTT; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.V[j][lane * 4]);
+        float p[kRW];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = p[i] < 0.f ? acc[i] : fmaf(p[i], v, acc[i]);
+        for (int i = 0; i < kRW; i += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(&sm.P[j][kRW * warp + i]);
+          p[i] = x.x;
+          p[i + 1] = x.y;
+        }
+#pragma unroll
+        for (int i = 0; i < kRW; ++i) {
+          acc[i][0] = fmaf(p[i], v.x, acc[i][0]);
+          acc[i][1] = fmaf(p[i], v.y, acc[i][1]);
+          acc[i][2] = fmaf(p[i], v.z, acc[i][2]);
+          acc[i][3] = fmaf(p[i], v.w, acc[i][3]);
+        }
+      }
     }
     bad = __syncthreads_or(bad_page);                  // the same answer for all: nobody looks at the next tile yet
   }
-  if (lane < 2) {
-    const int r = 2 * warp + lane;
-    // a sequence that could not be read is NaN, not a guess
-    ml[2 * r] = bad ? __uint_as_float(kTreeBadPart) : m[lane];
-    ml[2 * r + 1] = bad ? __int_as_float(0x7fc00000) : l[lane];
-  }
-  float* o = a.part + ((unit * a.parts + part) * kRB + 8 * half) * kD + d_o;
+  float* o = a.part + ((unit * a.parts + part) * kRB + kRW * warp) * kD + lane * 4;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i * kD] = acc[i];
+  for (int i = 0; i < kRW; ++i) {
+    const int r = kRW * warp + i;
+    if (lane == 0) {
+      // a sequence that could not be read is NaN, not a guess
+      ml[2 * r] = bad ? __uint_as_float(kTreeBadPart) : m[i];
+      ml[2 * r + 1] = bad ? __int_as_float(0x7fc00000) : l[i];
+    }
+    *reinterpret_cast<float4*>(o + i * kD) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  }
 }
 
-}  // namespace
-
-void tree_plan_simt(const Plan& pl, TreePlan* tp) {
-  tp->RB = kRB;
-  tp->n_blk = (tp->rows + kRB - 1) / kRB;
-  // parts so that two CTAs an SM have work, of a tile at least
-  const int64_t units = (int64_t)tp->batch * pl.H * tp->n_blk, tiles = (pl.N + tp->cap + tp->T + kTT - 1) / kTT;
-  tp->parts = tp->tail_parts = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (2 * 148 + units - 1) / units));
-}
-
-int launch_tree_simt(const TreeArgs& a, cudaStream_t s) {
+template <int RB>
+int launch_rb(const TreeArgs& a, cudaStream_t s) {
   static std::mutex mu;
   static int ready_dev = -1;
   int dev = 0;
@@ -257,15 +296,30 @@ int launch_tree_simt(const TreeArgs& a, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (ready_dev != dev) {
-      if (cudaFuncSetAttribute(tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Sm)) !=
+      if (cudaFuncSetAttribute(tree_simt_kernel<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Sm<RB>)) !=
           cudaSuccess)
         return ANCHORKV_ECUDA;
       ready_dev = dev;
     }
   }
-  tree_simt_kernel<<<dim3(a.parts, a.n_blk, a.batch * a.H), kThr, sizeof(Sm), s>>>(a);
+  tree_simt_kernel<RB><<<dim3(a.parts, a.n_blk, a.batch * a.H), kThr, sizeof(Sm<RB>), s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
-  return launch_tree_merge<float>(a, kRB, s);
+  return launch_tree_merge<float>(a, RB, s);
 }
+
+}  // namespace
+
+void tree_plan_simt(const Plan& pl, TreePlan* tp) {
+  // 64 rows where they fill the SMs too
+  const int64_t tiles = (pl.N + tp->cap + tp->T + kTT - 1) / kTT;
+  const bool wide = tp->rows > 16 && (int64_t)tp->batch * pl.H * ((tp->rows + 63) / 64) * tiles >= 2 * 148;
+  tp->RB = wide ? 64 : 16;
+  tp->n_blk = (tp->rows + tp->RB - 1) / tp->RB;
+  // parts so that two CTAs an SM have work, of a tile at least
+  const int64_t units = (int64_t)tp->batch * pl.H * tp->n_blk;
+  tp->parts = tp->tail_parts = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (2 * 148 + units - 1) / units));
+}
+
+int launch_tree_simt(const TreeArgs& a, cudaStream_t s) { return a.RB == 16 ? launch_rb<16>(a, s) : launch_rb<64>(a, s); }
 
 }  // namespace akv

@@ -271,6 +271,49 @@ def test_magnitudes(dtype, scale):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [1, 8, 40])
+@pytest.mark.parametrize("up", [True, False])
+def test_logits_and_values_that_keep_growing(dtype, T, up):
+    """Every tile's logits and values are larger than all before (or smaller), by far more than a reference holds."""
+    pr = Problem(dtype=dtype, T=T, B=1, lens=[1500], page=64, N=300, q_scale=1.0)
+    table = api.pages_view(pr.pages, pr.state)["table"][0]
+    g = torch.Generator().manual_seed(3)
+    u = torch.randn(D, generator=g)
+    q = pr.q.float()
+    pr.q = (0.3 * q + u).to(pr.p.torch_dtype)
+    for j, page in enumerate(table.tolist()):
+        step = j if up else len(table) - j
+        pr.Kp[page] = (0.05 * pr.Kp[page].float() + step * u).to(pr.p.torch_dtype)
+        pr.Vp[page] = (pr.Vp[page].float() * 2.0 ** (3 * step)).to(pr.p.torch_dtype)
+    got = pr.call().cpu().double()
+    want, tol = pr.expect()
+    assert ((got - want).norm(dim=3) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_infinity_in_a_committed_value(dtype):
+    """All rows see it: its coordinate is not finite, the others are what they were."""
+    pr = Problem(dtype=dtype, T=4, B=2, lens=[20, 9])
+    clean = pr.call()
+    page = int(api.pages_view(pr.pages, pr.state)["table"][0, 1])
+    pr.Vp[page, 1, 2, 100] = float("inf")
+    got = pr.call()
+    heads = slice(pr.G, 2 * pr.G)
+    assert not torch.isfinite(got[0, :, heads, 100]).any()
+    got[0, :, heads, 100] = clean[0, :, heads, 100]
+    assert torch.equal(got, clean)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_beams_of_one_prompt(dtype):
+    """More sequences than a warp has lanes, on one layout, with tails of every length."""
+    Problem(dtype=dtype, H=1, G=2, N=400, B=37, layouts=1, T=2, lens=[3 * b for b in range(37)]).check()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_strided_inputs(dtype):
     """Slices of one fused projection, as a model produces them, and padded batches."""
     pr = Problem(dtype=dtype, T=5, B=3, lens=[3, 20, 0])
@@ -468,7 +511,7 @@ def host_call(p=None, ws=FAKE, ws_bytes=1 << 40, **over):
 
 @pytest.mark.parametrize("over,status", [
     (dict(batch=-1), capi.EINVAL), (dict(n_draft=0), capi.EINVAL), (dict(n_draft=65), capi.EINVAL),
-    (dict(batch=40000), capi.EUNSUPPORTED), (dict(q=None), capi.EINVAL), (dict(K_new=None), capi.EINVAL),
+    (dict(batch=40000), capi.EUNSUPPORTED), (dict(batch=1, p=api.AnchorKVParams(n_tokens=100, n_kv_heads=32768, n_q_heads=32768)), capi.EUNSUPPORTED), (dict(q=None), capi.EINVAL), (dict(K_new=None), capi.EINVAL),
     (dict(V_new=None), capi.EINVAL), (dict(out=None), capi.EINVAL), (dict(ws=None), capi.EINVAL),
     (dict(n_layouts=1), capi.EINVAL), (dict(n_layouts=0, layout_of=FAKE), capi.EINVAL),
     (dict(seq_stride_bytes=1 << 10), capi.EINVAL), (dict(seq_stride_bytes=(1 << 20) + 8), capi.EINVAL),
