@@ -17,9 +17,12 @@
 // never matters: every row, of an anchor, a query or an exact token, is
 // divided by a power of two near its largest element, and what a token row is
 // multiplied by,
-//   row_t = x^_t / w_t,    w_t = gamma_t M_a  (or sigma_t where that is larger),
+//   row_t = x^_t / w_t,    w_t = gamma_t M_a,
 // is applied in fp32, to the logits for keys and to the probabilities for
-// values.  Accumulators, logits and sums are fp32.
+// values; a residual's row is then its anchor's plus its levels times
+// sigma_t / w_t.  (Where gamma_t M_a is below 2^-14 sigma_t, w_t is
+// 2^-14 sigma_t: the row stays in range, and the anchor's share, wrong by at
+// most twice that, is below the rounding of the row.)  Accumulators, logits and sums are fp32.
 //
 // One CTA owns up to 64 rows (draft, query head) of one (sequence, KV head)
 // and a share of its tokens, in tiles of 128:
@@ -70,11 +73,11 @@ constexpr float kRefGap = 120.f;          // the references' largest distance do
 
 // What a tile of one side needs beside rows and codes, written by the
 // pre-kernel: per token its scale and its anchor slot; per residual record the
-// factors of its anchor and its levels (fp16, one of them 1) and its token;
-// `quarter`: byte q counts the records before quarter q.
+// factor of its levels (fp16) and its token; `quarter`: byte q counts the
+// records before quarter q.
 struct Table {
   uint16_t slot[kTT];
-  uint32_t fac[kTT];
+  uint16_t level[kTT];
   uint8_t tok[kTT];
   uint32_t quarter, n_rec, first, pad;
 };
@@ -118,7 +121,7 @@ struct Sm {
   alignas(16) Table meta[2][S::kMetaSl];  // [side]
   alignas(16) float rk[S::kKSl][kTT];     // key scales
   alignas(16) float wv[S::kVSl][kTT];     // value scales
-  uint32_t lut[16];                       // two codes -> their levels in fp16
+  alignas(64) uint32_t lut[16];           // two codes -> their levels in fp16
   alignas(16) float cs[kRows];            // per row: logit scale
   // per row and tile parity: -reference of the sum, 2^(reference of the sum -
   // that of w p), reference of w p
@@ -137,7 +140,7 @@ template <int NC>
 constexpr bool sm_aligned() {
   return offsetof(Sm<NC>, cs) % 16 == 0 && offsetof(Sm<NC>, nm) % 16 == 0 && offsetof(Sm<NC>, cw) % 16 == 0 &&
          offsetof(Sm<NC>, codes) % 16 == 0 && offsetof(Sm<NC>, meta) % 16 == 0 && offsetof(Sm<NC>, V) % 1024 == 0 &&
-         offsetof(Sm<NC>, P) % 1024 == 0 && offsetof(Sm<NC>, Q) % 1024 == 0;
+         offsetof(Sm<NC>, lut) % 64 == 0 && offsetof(Sm<NC>, P) % 1024 == 0 && offsetof(Sm<NC>, Q) % 1024 == 0;
 }
 static_assert(sm_aligned<16>() && sm_aligned<32>() && sm_aligned<64>() && sm_aligned<128>(), "16-byte reads, swizzle atoms");
 
@@ -243,6 +246,18 @@ __device__ __forceinline__ void commit_elected(uint64_t* bar) {
       : "memory");
 }
 
+// The Hadamard transform of fwht128 with one multiply-add a butterfly.
+__device__ __forceinline__ void fwht128_signed(float (&v)[4], int lane) {
+  const float a0 = v[0] + v[1], a1 = v[0] - v[1], a2 = v[2] + v[3], a3 = v[2] - v[3];
+  v[0] = a0 + a2; v[2] = a0 - a2; v[1] = a1 + a3; v[3] = a1 - a3;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const float s = lane & m ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaf(v[i], s, __shfl_xor_sync(0xffffffffu, v[i], m));
+  }
+}
+
 // First sequence with the layout of sequence b: it holds the rotated anchors.
 __device__ __forceinline__ int first_with_layout(const TreeArgs& a, int b) {
   if (!a.layout_of) return b;
@@ -284,7 +299,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
           const int d = 4 * lane + i;
           if ((a.sign_bits[d >> 5] >> (d & 31)) & 1u) v[k][i] = -v[k][i];
         }
-        fwht128(v[k]);
+        fwht128_signed(v[k], lane);
       }
       const float m = warp_max(fmaxf(fmaxf(fabsf(v[k][0]), fabsf(v[k][1])), fmaxf(fabsf(v[k][2]), fabsf(v[k][3]))));
       const int e = scale_exp(__float_as_uint(m)), row = k ? s1 : s;
@@ -296,83 +311,70 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   }
 }
 
-constexpr int kMetaTiles = 4;
-
-// Token tables of every layout in use, one warp per 32 tokens of a side and
-// head, after the anchors' scales: what a token row is multiplied by,
-// w_t = gamma_t M_a or sigma_t where that is larger, and a residual row's
-// factors (one of the two is 1).  Bound by latency and the tables' writes
-// (2 KB a tile and side).
+// Token tables of every layout in use, one warp per tile of a side and head,
+// after the anchors' scales.  A lane has a token of each quarter, so that what a
+// tile's records have in common is found once (four warps a tile and a quarter
+// each took 279 instructions a quarter).  Bound by latency for one sequence, by
+// the tables' writes (1.2 KB a tile and side) for many.
 __global__ void __launch_bounds__(256) tree_meta_kernel(TreeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kTiles = kMetaTiles;                     // a warp's tiles, their loads in flight together
-  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, b = blockIdx.z, sh = blockIdx.y;
+  const int lane = threadIdx.x & 31, b = blockIdx.z, sh = blockIdx.y, tile = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lay = tree_layout(a, b);
-  if (lay < 0 || first_with_layout(a, b) != b) {
+  if (tile >= a.n_tiles || lay < 0 || first_with_layout(a, b) != b) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // this kernel is over after the one before it
     return;
   }
   const uint8_t* comp = a.comp + (int64_t)lay * a.stride;
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(comp + a.off_tok) + (int64_t)sh * a.N;
-  const uint4* bms = reinterpret_cast<const uint4*>(comp + a.off_bm) + (int64_t)sh * a.n_tiles;
-  const int* pfs = reinterpret_cast<const int*>(comp + a.off_pf) + (int64_t)sh * (a.n_tiles + 1);
-  const uint16_t* sig = reinterpret_cast<const uint16_t*>(comp + a.off_sig);
-  const int tile0 = (blockIdx.x * 2 + (threadIdx.x >> 7)) * kTiles;
-  uint32_t word[kTiles];
-  uint4 bm[kTiles];
-  int first[kTiles];
+  const int64_t tile_sh = (int64_t)sh * a.n_tiles + tile;
+  const uint4 bm = *reinterpret_cast<const uint4*>(comp + a.off_bm + tile_sh * 16);
+  const int first = reinterpret_cast<const int*>(comp + a.off_pf)[tile_sh + sh];
+  const int left = a.N - tile * kTT;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(comp + a.off_tok) + (int64_t)sh * a.N + tile * kTT + lane;
+  uint32_t word[4], bits[4] = {bm.x, bm.y, bm.z, bm.w};
+  int before[5] = {0};
 #pragma unroll
-  for (int k = 0; k < kTiles; ++k) {
-    const int tile = tile0 + k, t = tile * kTT + q * 32 + lane;
-    word[k] = t < a.N ? words[t] : 0u;
-    bm[k] = tile < a.n_tiles ? bms[tile] : make_uint4(0u, 0u, 0u, 0u);
-    first[k] = tile < a.n_tiles ? pfs[tile] : 0;
+  for (int q = 0; q < 4; ++q) {
+    word[q] = q * 32 + lane < left ? words[q * 32] : 0u;
+    // bits behind the last token mean nothing
+    if (left < 32 * q + 32) bits[q] &= left > 32 * q ? (1u << (left - 32 * q)) - 1u : 0u;
+    before[q + 1] = before[q] + __popc(bits[q]);
   }
-  float sg[kTiles];
-  int x[kTiles], before[kTiles][4];
-  bool res[kTiles], fine[kTiles];
+  const bool fine = first >= 0 && first + (int64_t)before[4] <= a.R;   // records outside the layout are none
+  const uint16_t* sig = reinterpret_cast<const uint16_t*>(comp + a.off_sig) + first;
+  const uint32_t below = (1u << lane) - 1u;
+  uint16_t sigma[4];
 #pragma unroll
-  for (int k = 0; k < kTiles; ++k) {
-    // bits behind the last token mean nothing, records outside the layout are none
-    uint32_t bits[4] = {bm[k].x, bm[k].y, bm[k].z, bm[k].w};
-    const int left = a.N - (tile0 + k) * kTT;
-    int sum = 0;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      if (left < 32 * y + 32) bits[y] &= left > 32 * y ? (1u << (left - 32 * y)) - 1u : 0u;
-      sum += __popc(bits[y]);
-      before[k][y] = sum;
-    }
-    fine[k] = first[k] >= 0 && first[k] + (int64_t)sum <= a.R;
-    const uint32_t mine = q == 0 ? bits[0] : q == 1 ? bits[1] : q == 2 ? bits[2] : bits[3];
-    x[k] = (q == 0 ? 0 : q == 1 ? before[k][0] : q == 2 ? before[k][1] : before[k][2]) + __popc(mine & ((1u << lane) - 1u));
-    res[k] = fine[k] && ((mine >> lane) & 1u);
-    sg[k] = res[k] ? half_bits_to_f(sig[first[k] + x[k]]) : 0.f;
+  for (int q = 0; q < 4; ++q) {
+    if (!fine) bits[q] = 0u;
+    sigma[q] = (bits[q] >> lane) & 1u ? sig[before[q] + __popc(bits[q] & below)] : (uint16_t)0;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* scale = a.anc_scale + ((int64_t)b * 2 * a.H + sh) * a.k;
-  float m[kTiles];
+  Meta& o = reinterpret_cast<Meta*>(a.meta)[(int64_t)b * 2 * a.H * a.n_tiles + tile_sh];
+  float m[4];
 #pragma unroll
-  for (int k = 0; k < kTiles; ++k) m[k] = scale[min((int)(word[k] & 0xffffu), a.k - 1)];
-  Meta* out = reinterpret_cast<Meta*>(a.meta) + ((int64_t)b * 2 * a.H + sh) * a.n_tiles;
+  for (int q = 0; q < 4; ++q) {
+    const int slot = min((int)(word[q] & 0xffffu), a.k - 1);
+    m[q] = scale[slot];
+    o.table.slot[q * 32 + lane] = (uint16_t)slot;
+  }
 #pragma unroll
-  for (int k = 0; k < kTiles; ++k) {
-    if (tile0 + k >= a.n_tiles) break;
-    Meta& o = out[tile0 + k];
-    const float c1 = half_bits_to_f(word[k] >> 16) * m[k];
-    const float sc = fabsf(c1) >= sg[k] ? c1 : sg[k], inv = sc != 0.f ? __fdividef(1.f, sc) : 0.f;
-    o.scale[q * 32 + lane] = sc;                         // 0 behind the last token, whose word is 0
-    o.table.slot[q * 32 + lane] = (uint16_t)min((int)(word[k] & 0xffffu), a.k - 1);
-    if (res[k]) {
-      o.table.fac[x[k]] = pack_half2(c1 * inv, sg[k] * inv);
-      o.table.tok[x[k]] = (uint8_t)(q * 32 + lane);
-    }
-    if (q == 0 && lane == 0) {
-      const uint32_t* f = reinterpret_cast<const uint32_t*>(before[k]);
-      *reinterpret_cast<uint4*>(&o.table.quarter) =
-          fine[k] ? make_uint4(f[0] << 8 | f[1] << 16 | f[2] << 24, f[3], (uint32_t)first[k], 0u) : make_uint4(0u, 0u, 0u, 0u);
+  for (int q = 0; q < 4; ++q) {
+    const float c1 = half_bits_to_f(word[q] >> 16) * m[q];             // 0 behind the last token, whose word is 0
+    const float sg = half_bits_to_f(sigma[q]);
+    const bool tiny = sg > fabsf(c1) * 16384.f;
+    o.scale[q * 32 + lane] = tiny ? sg * (1.f / 16384.f) : c1;
+    if ((bits[q] >> lane) & 1u) {
+      const int x = before[q] + __popc(bits[q] & below);
+      o.table.level[x] = __half_as_ushort(__float2half_rn(tiny ? 16384.f : c1 != 0.f ? __fdividef(sg, c1) : 0.f));
+      o.table.tok[x] = (uint8_t)(q * 32 + lane);
     }
   }
+  if (lane == 0)
+    *reinterpret_cast<uint4*>(&o.table.quarter) =
+        fine ? make_uint4((uint32_t)before[1] << 8 | (uint32_t)before[2] << 16 | (uint32_t)before[3] << 24, (uint32_t)before[4],
+                          (uint32_t)first, 0u)
+             : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Waits for a phase.  A phase that is over already, the usual case in a full
@@ -416,10 +418,13 @@ __device__ __forceinline__ uint64_t* scales_bar(M& sm, int side, int t) {
   return side ? &sm.sv[t % M::S::kVSl] : &sm.sk[t % M::S::kKSl];
 }
 
-// x = ca x + cb level, two coordinates.
-__device__ __forceinline__ void add_levels(uint32_t& x, __half2 ca, __half2 cb, uint32_t level) {
-  const __half2 r = __hfma2(cb, *reinterpret_cast<const __half2*>(&level), __hmul2(ca, *reinterpret_cast<const __half2*>(&x)));
-  x = *reinterpret_cast<const uint32_t*>(&r);
+// x + factor times the levels at shared address `at`, two coordinates.
+__device__ __forceinline__ uint32_t add_levels(uint32_t x, uint32_t factor, uint32_t at) {
+  uint32_t lev;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(lev) : "r"(at));
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&factor), *reinterpret_cast<const __half2*>(&lev),
+                            *reinterpret_cast<const __half2*>(&x));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Token tables and codes of one side, by one lane, as far ahead as there are
@@ -463,6 +468,7 @@ __device__ void produce_prefix(const TreeArgs& a, M& sm, int w, int n, const uin
   const Lane me = lane_of<M::S::kProd>(w);
   const int lane = threadIdx.x & 31, c = lane & 15, hw = lane >> 4, c8 = lane & 7, g = lane >> 3;
   rows += c * 16;
+  const uint32_t lut = tc::smem_u32(sm.lut);             // 64-byte aligned
   for (int t = me.first; t < n; t += me.step) {
     wait_b(sm, &sm.loaded[me.side][t % kMetaSl], (t / kMetaSl) & 1, a);
     const Table* m = &sm.meta[me.side][t % kMetaSl];
@@ -491,13 +497,13 @@ __device__ void produce_prefix(const TreeArgs& a, M& sm, int w, int n, const uin
     for (int x = x0 + g; x < x1; x += 8) {
       const bool two = x + 4 < x1;
       uint8_t* row[2];
-      uint32_t f[2], code[2][2];
+      uint32_t code[2][2], lv[2];
       uint4 v[2][2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int y = k && two ? x + 4 : x;
-        const uint32_t tk = m->tok[y];
-        f[k] = m->fac[y];
+        const uint32_t tk = m->tok[y], f = m->level[y];
+        lv[k] = __byte_perm(f, 0u, 0x1010u);
         row[k] = tile + tk * 128 + ((c8 ^ (tk & 7u)) << 4);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -508,12 +514,13 @@ __device__ void produce_prefix(const TreeArgs& a, M& sm, int w, int n, const uin
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (k && !two) break;
-        const __half2 f2 = *reinterpret_cast<const __half2*>(&f[k]), ca = __low2half2(f2), cb = __high2half2(f2);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          uint32_t* vw = reinterpret_cast<uint32_t*>(&v[k][p]);
-#pragma unroll
-          for (int z = 0; z < 4; ++z) add_levels(vw[z], ca, cb, sm.lut[(code[k][p] >> (4 * z)) & 15u]);
+          const uint32_t c = code[k][p] << 2;            // two codes' table entry: four bits of c at 4 z + 2
+          v[k][p].x = add_levels(v[k][p].x, lv[k], lut | (c & 60u));
+          v[k][p].y = add_levels(v[k][p].y, lv[k], lut | ((c >> 4) & 60u));
+          v[k][p].z = add_levels(v[k][p].z, lv[k], lut | ((c >> 8) & 60u));
+          v[k][p].w = add_levels(v[k][p].w, lv[k], lut | ((c >> 12) & 60u));
           *reinterpret_cast<uint4*>(row[k] + p * kHalf) = v[k][p];
         }
       }
@@ -815,7 +822,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         const int d = 4 * lane + i;
         if ((a.sign_bits[d >> 5] >> (d & 31)) & 1u) v[i] = -v[i];
       }
-      fwht128(v);
+      fwht128_signed(v, lane);
     }
     const float m = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
     const int e = scale_exp(__float_as_uint(m));
@@ -1088,7 +1095,7 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
   int st = ANCHORKV_OK;
-  if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 2 * kMetaTiles - 1) / (2 * kMetaTiles), 2 * a.H, a.batch), 256, 0, s, a);
+  if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 7) / 8, 2 * a.H, a.batch), 256, 0, s, a);
   if (st) return st;
   st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, smem_bytes<NC>(), s, a);
   if (st) return st;

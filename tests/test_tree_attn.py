@@ -292,6 +292,32 @@ def test_logits_and_values_that_keep_growing(dtype, T, up):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("gamma", [0.0, 6e-8, 1e-5, 1e-3, -1.0, "by token"])
+@pytest.mark.parametrize("sigma", [0.0, 1.0, 6e4])
+def test_scales_of_tokens_and_residuals(dtype, gamma, sigma):
+    """Layouts whose anchors or residuals weigh next to nothing, or all there is, or count backwards."""
+    pr = Problem(dtype=dtype, T=3, B=1, N=700, theta=0.4, lens=[9], q_scale=1.0)
+    po = O.Params(n_tokens=700, n_kv_heads=pr.H, n_q_heads=pr.H * pr.G, theta=0.4, dtype=dtype)
+    off, N, R = O.layout(po)["off"], po.n_tokens, O.layout(po)["R"]
+    image = pr.comp[0].cpu().numpy()
+    tok = image[off["tok"]:off["tok"] + 8 * pr.H * N].view(np.uint32)
+    g16 = np.float16([0.0, 6e-8, 1e-5, 1e-3, -1.0, 1.0, 30.0])[np.arange(len(tok)) % 7] if gamma == "by token" \
+        else np.full(len(tok), gamma, np.float16)
+    tok[:] = tok & 0xFFFF | g16.view(np.uint16).astype(np.uint32) << 16
+    sig = image[off["res_sigma"]:off["res_sigma"] + 2 * R].view(np.float16)
+    sig[:] = (sig.astype(np.float64) * sigma).clip(0, 6e4).astype(np.float16)
+    pr.comp[0] = torch.tensor(image)
+    parts = O.unpack_layout(image, po)
+    full, bare = O.reconstruct(parts, po), O.reconstruct(dict(parts, codes=np.zeros((0, D), np.uint8)), po)
+    pr.dense[0] = [(torch.tensor(f), torch.tensor(np.linalg.norm(a, axis=-1) + np.linalg.norm(f - a, axis=-1)))
+                   for f, a in zip(full, bare)]
+    got = pr.call().cpu().double()
+    want, tol = pr.expect()
+    assert torch.isfinite(got).all() and ((got - want).norm(dim=3) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_infinity_in_a_committed_value(dtype):
     """All rows see it: its coordinate is not finite, the others are what they were."""
     pr = Problem(dtype=dtype, T=4, B=2, lens=[20, 9])
