@@ -596,6 +596,7 @@ int anchorkv_pages_commit(const anchorkv_pages* pg, const int32_t* state_in, int
   if (st) return st;
   if (batch < 0 || batch > a.S || n_draft < 1 || n_draft > 65536 || !n_accept) return ANCHORKV_EINVAL;
   if (!K_new || !V_new || (((uintptr_t)K_new | (uintptr_t)V_new) & 15)) return ANCHORKV_EINVAL;
+  if (((uintptr_t)path | (uintptr_t)n_accept) & 3) return ANCHORKV_EINVAL;
   st = op_args(pg, state_in, state_out, K_pages, V_pages, ws, ws_bytes, &a);
   if (st) return st;
   a.fresh[0] = (const uint4*)K_new; a.fresh[1] = (const uint4*)V_new;
@@ -615,7 +616,7 @@ int anchorkv_pages_commit(const anchorkv_pages* pg, const int32_t* state_in, int
 int anchorkv_pages_fork(const anchorkv_pages* pg, const int32_t* state_in, int32_t* state_out, void* K_pages,
                         void* V_pages, const int32_t* parents, void* ws, size_t ws_bytes, void* stream) {
   PgArgs a;
-  if (!parents) return ANCHORKV_EINVAL;
+  if (!parents || ((uintptr_t)parents & 3)) return ANCHORKV_EINVAL;
   int st = op_args(pg, state_in, state_out, K_pages, V_pages, ws, ws_bytes, &a);
   if (st) return st;
   a.parents = parents;

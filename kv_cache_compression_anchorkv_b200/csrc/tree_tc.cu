@@ -739,7 +739,10 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   const int64_t unit = (int64_t)bh * a.n_blk + blk;
   float* ml = a.ml + (unit * a.parts + part) * NC * 2;
   const int n_new = tree_new(a, b), rows = n_new * a.G;
-  if (blk * NC >= rows) return;                       // nobody reads these parts
+  if (blk * NC >= rows) {                             // nobody reads these parts
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // this kernel is over after those before it
+    return;
+  }
   // this part's tiles: the first parts take the exact tokens, the others the compressed
   const bool tail = part < a.tail_parts;
   const int lay = a.comp ? tree_layout(a, b) : 0, len = tree_len(a, b);

@@ -349,3 +349,13 @@ def test_bad_fork_arguments_refused(at, value, status):
     if at != 4:
         del args[4]
         assert call("anchorkv_pages_compact", ctypes.byref(spec.c()), *args, None) == status
+
+
+def test_unaligned_indices_refused():
+    spec = api.PageSpec(n_pages=8, n_slots=4)
+    for at in (8, 9):
+        args = [FAKE, FAKE, FAKE + 4096, FAKE + 8192, FAKE, FAKE, 4, 2, FAKE, FAKE, FAKE, 1 << 20]
+        args[at] = FAKE + 2
+        assert call("anchorkv_pages_commit", ctypes.byref(spec.c()), *args, None) == capi.EINVAL
+    args = [FAKE, FAKE, FAKE + 4096, FAKE + 8192, FAKE + 2, FAKE, 1 << 20]
+    assert call("anchorkv_pages_fork", ctypes.byref(spec.c()), *args, None) == capi.EINVAL
