@@ -259,12 +259,25 @@ __device__ __forceinline__ void fwht128_signed(float (&v)[4], int lane) {
 }
 
 // First sequence with the layout of sequence b: it holds the rotated anchors.
+// By a whole warp.
 __device__ __forceinline__ int first_with_layout(const TreeArgs& a, int b) {
   if (!a.layout_of) return b;
-  const int mine = a.layout_of[b];
-  for (int i = 0; i < b; ++i)
-    if (a.layout_of[i] == mine) return i;
+  const int mine = a.layout_of[b], lane = threadIdx.x & 31;
+  for (int i = 0; i < b; i += 32) {
+    const uint32_t same = __ballot_sync(0xffffffffu, i + lane < b && a.layout_of[i + lane] == mine);
+    if (same) return i + __ffs((int)same) - 1;
+  }
   return b;
+}
+
+// Bits 0..3: the signs that the rotation flips of this lane's four coordinates.
+__device__ __forceinline__ uint32_t flipped(const TreeArgs& a, int lane) {
+  const uint32_t lo = lane & 8 ? a.sign_bits[1] : a.sign_bits[0], hi = lane & 8 ? a.sign_bits[3] : a.sign_bits[2];
+  return (lane & 16 ? hi : lo) >> ((4 * lane) & 31) & 15u;
+}
+__device__ __forceinline__ void flip(float (&v)[4], uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) ^ ((bits << (31 - i)) & 0x80000000u));
 }
 
 // Rotated anchors of every layout in use, one warp per row: fp16 rows over a
@@ -286,6 +299,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
       reinterpret_cast<const __nv_bfloat16*>(a.comp + (int64_t)lay * a.stride + (side ? a.off_av : a.off_ak)) +
       (int64_t)h * a.k * kD;
   const int64_t row0 = ((int64_t)b * 2 * a.H + sh) * a.k;
+  const uint32_t signs = flipped(a, lane);
+  const float unit = a.naive ? 1.f : rsqrtf((float)kD);
   for (int s = (blockIdx.x * 8 + warp) * 2; s < a.k; s += gridDim.x * 16) {
     const int s1 = min(s + 1, a.k - 1);                  // two rows' latencies together
     float v[2][4];
@@ -294,11 +309,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!a.naive) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = 4 * lane + i;
-          if ((a.sign_bits[d >> 5] >> (d & 31)) & 1u) v[k][i] = -v[k][i];
-        }
+        flip(v[k], signs);
         fwht128_signed(v[k], lane);
       }
       const float m = warp_max(fmaxf(fmaxf(fabsf(v[k][0]), fabsf(v[k][1])), fmaxf(fabsf(v[k][2]), fabsf(v[k][3]))));
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
       const float inv = exp_to_inv(e);
       reinterpret_cast<uint2*>(a.anc)[(row0 + row) * 32 + lane] =
           make_uint2(pack_half2(v[k][0] * inv, v[k][1] * inv), pack_half2(v[k][2] * inv, v[k][3] * inv));
-      if (lane == 0) a.anc_scale[row0 + row] = exp_to_f(e) * (a.naive ? 1.f : rsqrtf((float)kD));
+      if (lane == 0) a.anc_scale[row0 + row] = exp_to_f(e) * unit;
     }
   }
 }
@@ -790,7 +801,10 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     }
     tc::fence_barrier_init();
   }
-  if (tid == 32) sm.rep = first_with_layout(a, b);
+  if (warp == 1) {
+    const int rep = first_with_layout(a, b);
+    if (lane == 0) sm.rep = rep;
+  }
   if (tail && warp == 2) {                            // the masks' columns
     const unsigned long long lo = lane < n_new ? tree_mask(a, b, lane) : 0ull;
     const unsigned long long hi = lane + 32 < n_new ? tree_mask(a, b, lane + 32) : 0ull;
@@ -813,6 +827,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     sm.lut[tid & 15] = pack_half2(lev(tid & 3), lev((tid >> 2) & 3));
   }
   const bool rotate = !tail && !a.naive;
+  const uint32_t signs = flipped(a, lane);
   for (int c = warp; c < NC; c += kThreads / 32) {
     const int r = blk * NC + c;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -820,11 +835,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       load4<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.q) + b * a.q_seq + (r / a.G) * a.q_tok +
                                (h * a.G + r % a.G) * kD + lane * 4, v);
     if (rotate) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = 4 * lane + i;
-        if ((a.sign_bits[d >> 5] >> (d & 31)) & 1u) v[i] = -v[i];
-      }
+      flip(v, signs);
       fwht128_signed(v, lane);
     }
     const float m = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
@@ -1094,7 +1105,8 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
       ready_dev = dev;
     }
   }
-  const int gx = a.comp ? std::max(1, std::min((a.k + 15) / 16, 256)) : 1;
+  // two rows a warp, or, of many sequences, as many as keep eight CTAs an SM busy
+  const int gx = a.comp ? std::max(1, std::min((a.k + 15) / 16, std::max(4, 148 * 16 / (2 * a.H * a.batch)))) : 1;
   tree_prep_kernel<<<dim3(gx, 2 * a.H, a.batch), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ANCHORKV_ECUDA;
   int st = ANCHORKV_OK;
