@@ -22,20 +22,23 @@
 // values; a residual's row is then its anchor's plus its levels times
 // sigma_t / w_t.  (Where gamma_t M_a is below 2^-14 sigma_t, w_t is
 // 2^-14 sigma_t: the row stays in range, and the anchor's share, wrong by at
-// most twice that, is below the rounding of the row.)  Accumulators, logits and sums are fp32.
+// most twice that, is below the rounding of the row.)  Accumulators, logits
+// and sums are fp32.
 //
-// One CTA owns up to 64 rows (draft, query head) of one (sequence, KV head)
-// and a share of its tokens, in tiles of 128:
+// One CTA owns 16, 32, 64 or 128 rows (draft, query head) of one (sequence, KV
+// head) and a share of its tokens, in tiles of 128:
 //   S^T [128 tokens x rows]  = K^ Q^T      A = key tile, B = queries
 //   O^T [128 coords x rows] += V^T P       A = value tile (token-major), B = P
 // Tokens are on the accumulator's lanes, so a thread owns a token: its scales
 // are scalars, its row of P is contiguous, and the cost of the softmax goes
-// with the rows there are (16, 32 or 64 columns) instead of a padded 128.
-//   softmax, 8 warps (16 for 64 rows): logits from tensor memory, exponentials,
-//     P to shared memory; at the end the outputs
-//   one warp issues the MMAs
-//   16 or 8 warps fill key and value tiles, 32 rows each: anchor rows by
-//     16-byte asynchronous copies into the 128-byte swizzle, residual rows
+// with the rows there are (16, 32, 64 or 128 columns) instead of a padded 128.
+//   8 or 16 softmax warps: logits from tensor memory, exponentials, P to shared
+//     memory; at the end the outputs
+//   one warp issues the logits' MMAs, one the outputs', so that the keys of a
+//     tile need not wait for the values of the one before
+//   two warps load token tables and codes ahead (bulk copies)
+//   16 or 8 producer warps fill key and value tiles, 32 rows each: anchor rows
+//     by 16-byte asynchronous copies into the 128-byte swizzle, residual rows
 //     finished in place (eight lanes each)
 // The maximum over tokens would need a reduction across lanes for every row
 // and tile.  Instead each row keeps two power-of-two references, one for the
@@ -43,7 +46,23 @@
 // would leave their range: one vote per tile.  Powers of two make every
 // rescaling exact, so the result does not depend on when it happens.
 //
-// Bound by the anchor rows' way from L2 (64 KB a tile).
+// Bound by instruction issue and the latency of the chain copy - residuals -
+// logits - softmax - outputs, not by memory or the tensor pipe.  For 16 rows a
+// tile costs about 4.6 k warp instructions (softmax 1 k, residual rows 1 k,
+// the rest copies and waits) and 2.2 k cycles; the anchor rows then come from
+// L2 at 6.5 TB/s (64 KB a tile).  For 128 rows it is the softmax: 16 warps, 11 k
+// warp instructions and 5 k cycles a tile, 56% of the issue slots.
+// Whole calls (CUDA graph, 8 KV heads, theta = 0.05), with the rate of
+// 4 D operations a row and token:
+//   32 k tokens, 32 query heads: 1 draft 34.9 us (205 GB/s of the layout: three
+//     fifths are the pre-kernels, the first tile and the merge), 16 drafts
+//     45.1 us (192 TFLOP/s), 64 drafts 116.6 us (304 TFLOP/s)
+//   128 k tokens, 64 query heads, 24 drafts: 338 us (306 TFLOP/s)
+//   16 sequences of 32 k tokens, theta = 0.1, 8 drafts: 519 us (487 GB/s)
+// Anchor rows by four-row TMA gathers were no faster than 16-byte copies (60.4
+// us against 59.8 on 16 drafts then: about 100 cycles of issue a gather);
+// finding the residuals' levels before the rows have landed was slower (36.5 ->
+// 39 us on one draft): the registers and second pass cost more than the wait.
 
 #include <stddef.h>
 
@@ -282,8 +301,9 @@ __device__ __forceinline__ void flip(float (&v)[4], uint32_t bits) {
 
 // Rotated anchors of every layout in use, one warp per row: fp16 rows over a
 // power of two and that power (1/sqrt(D) of the rotation in it).  Clears the
-// status words and the flags of infinite values.  Bound by launch latency
-// (4.6 k rows for a 32k-token prompt, 2.4 MB).
+// status words and the flags of infinite values.  Bound by launch latency for
+// one sequence (4.6 k rows of a 32 k-token prompt, 1.2 MB read: 2.5 us inside
+// the call); for many by instruction issue, about 140 a row (16 sequences: 16 us).
 __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.z, sh = blockIdx.y;
@@ -325,8 +345,10 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
 // Token tables of every layout in use, one warp per tile of a side and head,
 // after the anchors' scales.  A lane has a token of each quarter, so that what a
 // tile's records have in common is found once (four warps a tile and a quarter
-// each took 279 instructions a quarter).  Bound by latency for one sequence, by
-// the tables' writes (1.2 KB a tile and side) for many.
+// each took 279 instructions a quarter; four tokens in a row a lane was no
+// shorter and its stores diverge, 41 us against 36).  Bound by latency for one
+// sequence (3.4 us after the anchors' scales), by issue for many, 400
+// instructions a tile (16 sequences, 65 k tiles: 36 us).
 __global__ void __launch_bounds__(256) tree_meta_kernel(TreeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, b = blockIdx.z, sh = blockIdx.y, tile = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -1126,7 +1148,16 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
   // first references, outputs) and a tile of 16, 32, 64 or 128 rows the times
   // below (in tenths of a microsecond, measured over 32 k and 128 k tokens), so
   // the block and the split are those whose longest run of CTAs on an SM is
-  // shortest.
+  // shortest.  Larger blocks rebuild each tile for more rows; smaller ones leave
+  // less of a block empty and spread over more SMs.  Measured (8 KV heads, us):
+  //   rows a head, block of  16     32     64    128
+  //   24,  32 k tokens      51.6   39.1
+  //   64,  32 k             93.6   60.5   45.1
+  //   128, 32 k            178    112     72.3   70.4
+  //   256, 32 k            344    215    135    117
+  //   192, 128 k           873    540    337    389
+  //   32,  16 x 32 k       809    529    688
+  //   64,  16 x 32 k      1507    963    703
   constexpr int64_t kFixed = 6;
   constexpr int kRows[4] = {16, 32, 64, 128}, kTime[4] = {12, 14, 17, 29};
   const int pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (int)((tp->cap + tp->T + kTT - 1) / kTT);
