@@ -17,7 +17,7 @@ constexpr uint32_t kTreeBadPart = 0x7fc0bad0u;
 // tokens `parts` CTAs share.
 struct TreePlan {
   int batch, T, rows, RB, n_blk, parts;
-  int tail_parts;                    // of those, CTAs of exact tokens only (tensor-core kernel)
+  int tail_parts;                    // of those, CTAs of exact tokens only; 0: by the sequence's lengths
   int64_t cap;                       // exact tokens that the page tables can hold
   // workspace (bytes): status words, (max, sum) and outputs of every
   // part; tensor-core kernel: rotated anchors, their scales, token tables,
@@ -75,6 +75,16 @@ __device__ __forceinline__ int tree_len(const TreeArgs& a, int b) {
   if (!a.table) return 0;
   const int n = a.len[b];
   return n < 0 || n > (int64_t)a.maxp * a.P ? -1 : n;
+}
+// Parts of a sequence that take exact tokens only, the first ones: as many as
+// its exact tokens' share of all tiles (of 128), one at least for either kind.
+// The page tables may have room for far more tokens than a sequence has, so the
+// launch fixes the parts and each sequence divides them by its own length.
+__device__ __forceinline__ int tree_tail_parts(const TreeArgs& a, int len, int n_new) {
+  if (a.tail_parts) return a.tail_parts;
+  // 2^13 tail tiles and 2^12 parts at most
+  const uint32_t tail = (uint32_t)(max(len, 0) + n_new + 127) / 128u, all = tail + a.n_tiles;
+  return max(1, min((int)((tail * a.parts + all - 1) / all), a.parts - 1));
 }
 __device__ __forceinline__ unsigned long long tree_mask(const TreeArgs& a, int b, int t) {
   return a.mask ? a.mask[(int64_t)b * a.T + t] : (2ull << t) - 1;

@@ -26,7 +26,8 @@
 // and sums are fp32.
 //
 // One CTA owns 16, 32, 64 or 128 rows (draft, query head) of one (sequence, KV
-// head) and a share of its tokens, in tiles of 128:
+// head) and a share of its tokens - the first parts exact ones, the others
+// compressed ones, by the sequence's own lengths - in tiles of 128:
 //   S^T [128 tokens x rows]  = K^ Q^T      A = key tile, B = queries
 //   O^T [128 coords x rows] += V^T P       A = value tile (token-major), B = P
 // Tokens are on the accumulator's lanes, so a thread owns a token: its scales
@@ -54,11 +55,11 @@
 // warp instructions and 5 k cycles a tile, 56% of the issue slots.
 // Whole calls (CUDA graph, 8 KV heads, theta = 0.05), with the rate of
 // 4 D operations a row and token:
-//   32 k tokens, 32 query heads: 1 draft 34.9 us (205 GB/s of the layout: three
+//   32 k tokens, 32 query heads: 1 draft 33.7 us (212 GB/s of the layout: three
 //     fifths are the pre-kernels, the first tile and the merge), 16 drafts
-//     45.1 us (192 TFLOP/s), 64 drafts 116.6 us (304 TFLOP/s)
-//   128 k tokens, 64 query heads, 24 drafts: 338 us (306 TFLOP/s)
-//   16 sequences of 32 k tokens, theta = 0.1, 8 drafts: 519 us (487 GB/s)
+//     44.7 us (194 TFLOP/s), 64 drafts 116.5 us (304 TFLOP/s)
+//   128 k tokens, 64 query heads, 24 drafts: 336 us (308 TFLOP/s)
+//   16 sequences of 32 k tokens, theta = 0.1, 8 drafts: 523 us (483 GB/s)
 // Anchor rows by four-row TMA gathers were no faster than 16-byte copies (60.4
 // us against 59.8 on 16 drafts then: about 100 cycles of issue a gather);
 // finding the residuals' levels before the rows have landed was slower (36.5 ->
@@ -777,13 +778,13 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     return;
   }
   // this part's tiles: the first parts take the exact tokens, the others the compressed
-  const bool tail = part < a.tail_parts;
-  const int lay = a.comp ? tree_layout(a, b) : 0, len = tree_len(a, b);
+  const int lay = a.comp ? tree_layout(a, b) : 0, len = tree_len(a, b), tail_parts = tree_tail_parts(a, len, n_new);
+  const bool tail = part < tail_parts;
   const bool out_of_range = lay < 0 || len < 0;
   int tile0, n;
   {
     const int tiles = tail ? (max(len, 0) + n_new + kTT - 1) / kTT : a.n_tiles;
-    const int s = tail ? part : part - a.tail_parts, of = tail ? a.tail_parts : a.parts - a.tail_parts;
+    const int s = tail ? part : part - tail_parts, of = tail ? tail_parts : a.parts - tail_parts;
     tile0 = (int)((int64_t)tiles * s / of);
     n = (int)((int64_t)tiles * (s + 1) / of) - tile0;
   }
@@ -940,24 +941,23 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     for (int x = 0; x < 8; ++x) lacc[x] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int x = 0; x < CH; ++x) lred[x] = 0.f;
+    // tokens before `open` are seen by all rows, those behind by the drafts that
+    // may, `end` and more are none
+    const int open = tail ? len : a.N, end = tail ? len + n_new : a.N;
     for (int i = par; i < n; i += PG) {
       const int bf = i & 1;
       // what this token is, and who sees it
-      const int t = (tile0 + i) * kTT + tok;
-      bool special = false, live = true;
+      const bool special = (tile0 + i + 1) * kTT > open;
       unsigned long long vis = ~0ull;
-      if (tail) {
-        special = (tile0 + i + 1) * kTT > len;
-        live = t < len + n_new;
-        if (special && live && t >= len) {
-          const uint2 s = sm.seen[t - len];
+      if (special) {
+        const int t = (tile0 + i) * kTT + tok;
+        if (t >= end) {
+          vis = 0;
+        } else if (t >= open) {
+          const uint2 s = sm.seen[t - open];
           vis = (unsigned long long)s.y << 32 | s.x;
         }
-      } else {
-        special = (tile0 + i + 1) * kTT > a.N;
-        live = t < a.N;
       }
-      if (!live) vis = 0;
       wait_b(sm, &sm.sk[i % kKSl], (i / kKSl) & 1, a);
       wait_b(sm, &sm.sv[i % kVSl], (i / kVSl) & 1, a);
       const float rk = sm.rk[i % kKSl][tok], w = sm.wv[i % kVSl][tok];
@@ -1167,25 +1167,19 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
     // as many CTAs a unit as fill a whole number of waves
     const int first = std::max(1, (units * (prefix ? 2 : 1) + 147) / 148);
     for (int waves = first; waves < first + 16; ++waves) {
-      const int ctas = 148 * waves / units;
-      int s = 0, per = 8, t = 1;
-      if (prefix) {
-        s = std::min(pre, std::max(1, ctas - 1));
-        per = (pre + s - 1) / s;
-        t = (tail + std::max(per, 4) - 1) / std::max(per, 4);
-        s = std::min(pre, std::max(1, ctas - t));
-        per = (pre + s - 1) / s;
-      } else {
-        t = std::min(tail, std::max(1, ctas));
-        per = (tail + t - 1) / t;
+      const int parts = std::max(prefix ? 2 : 1, std::min(148 * waves / units, pre + tail));
+      int per = (tail + parts - 1) / parts;
+      if (prefix) {                        // as tree_tail_parts divides them
+        const int t = std::max(1, std::min((int)(((int64_t)tail * parts + pre + tail - 1) / (pre + tail)), parts - 1));
+        per = std::max((pre + parts - t - 1) / (parts - t), (tail + t - 1) / t);
       }
-      const int64_t cost = ((int64_t)units * (s + t) + 147) / 148 * (std::max(per, (tail + t - 1) / t) + kFixed) * kTime[k];
+      const int64_t cost = ((int64_t)units * parts + 147) / 148 * (per + kFixed) * kTime[k];
       if (cost < best) {
         best = cost;
         tp->RB = kRows[k];
         tp->n_blk = n_blk;
-        tp->parts = s + t;
-        tp->tail_parts = t;
+        tp->parts = parts;
+        tp->tail_parts = prefix ? 0 : parts;
       }
     }
   }

@@ -40,7 +40,7 @@ class Problem:
     """Layouts, pages and drafts of one call, with the dense rows in 64 bits."""
 
     def __init__(self, dtype="bf16", H=2, G=4, N=1500, theta=0.2, B=2, T=5, lens=None, page=16, layouts=None, mode=0,
-                 n_new=None, mask="tree", seed=1, q_scale=3.0, prefix=True, spare=2):
+                 n_new=None, mask="tree", seed=1, q_scale=3.0, prefix=True, spare=2, room=0):
         g = torch.Generator().manual_seed(seed)
         self.p = api.AnchorKVParams(n_tokens=N, n_kv_heads=H, n_q_heads=H * G, theta=theta, dtype=dtype, mode=mode)
         po = O.Params(n_tokens=N, n_kv_heads=H, n_q_heads=H * G, theta=theta, dtype=dtype, mode=mode)
@@ -78,7 +78,7 @@ class Problem:
         self.lens = lens or [0] * B
         if lens is not None:
             need = [-(-n // page) for n in lens]
-            n_pages, maxp = sum(need) + spare, max(max(need), 1)
+            n_pages, maxp = sum(need) + spare, max(max(need), 1) + room
             self.pages = api.PageSpec(n_pages=n_pages, page_size=page, n_slots=B, max_pages=maxp, n_kv_heads=H, dtype=dtype)
             ids = torch.randperm(n_pages, generator=g).tolist()
             state = torch.zeros(self.pages.state_numel, dtype=torch.int32)
@@ -178,6 +178,8 @@ CASES = {
     "drafts-only": dict(prefix=False, T=10, B=2),
     "flat-queries": dict(q_scale=0.01, lens=[9, 300]),
     "sharp-queries": dict(q_scale=20.0, lens=[9, 300]),
+    "room-in-the-tables": dict(T=3, B=3, lens=[3, 700, 0], page=64, room=500),
+    "room-and-a-short-prefix": dict(N=150, T=2, B=2, lens=[900, 1], page=16, room=3000),
     "long": dict(N=9000, B=1, T=8, lens=[1000], page=64, theta=0.1),
 }
 
