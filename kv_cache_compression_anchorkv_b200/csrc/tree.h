@@ -76,7 +76,7 @@ __device__ __forceinline__ int tree_len(const TreeArgs& a, int b) {
   const int n = a.len[b];
   return n < 0 || n > (int64_t)a.maxp * a.P ? -1 : n;
 }
-// Parts of a sequence that take exact tokens only, the first ones: as many as
+// Parts of a sequence that take exact tokens only, the last ones: as many as
 // its exact tokens' share of all tiles (of 128), one at least for either kind.
 // The page tables may have room for far more tokens than a sequence has, so the
 // launch fixes the parts and each sequence divides them by its own length.

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int rb) {
   const int b = there ? (int)(i / (a.T * Hq)) : 0, t = (int)(i / Hq % a.T), hq = (int)(i % Hq), h = hq / a.G;
   const bool wanted = there && t < tree_new(a, b);
   const unsigned long long seen = wanted && a.inf_v ? tree_mask(a, b, t) : 0ull;
-  const int tail_parts = wanted ? tree_tail_parts(a, tree_len(a, b), tree_new(a, b)) : 0;
+  const int prefix_parts = wanted ? a.parts - tree_tail_parts(a, tree_len(a, b), tree_new(a, b)) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!wanted) return;
   const int r = t * a.G + hq % a.G;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int rb) {
       l = l * f + e[k].y * g;
       x.x *= f; x.y *= f; x.z *= f; x.w *= f;
       y.x *= f; y.y *= f; y.z *= f; y.w *= f;
-      float4& z = s < tail_parts ? y : x;
+      float4& z = s < prefix_parts ? x : y;
       z.x = fmaf(v[k].x, g, z.x); z.y = fmaf(v[k].y, g, z.y); z.z = fmaf(v[k].z, g, z.z); z.w = fmaf(v[k].w, g, z.w);
     }
   }
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int rb) {
     c[0] = fmaf(p.x, f, c[0]); c[1] = fmaf(p.y, f, c[1]); c[2] = fmaf(p.z, f, c[2]); c[3] = fmaf(p.w, f, c[3]);
     d[0] = fmaf(q.x, f, d[0]); d[1] = fmaf(q.y, f, d[1]); d[2] = fmaf(q.z, f, d[2]); d[3] = fmaf(q.w, f, d[3]);
   }
-  if (!a.naive && tail_parts < a.parts) {
+  if (!a.naive && prefix_parts > 0) {
     fwht128(c);
     const float n = rsqrtf((float)kD);
 #pragma unroll

@@ -26,8 +26,8 @@
 // and sums are fp32.
 //
 // One CTA owns 16, 32, 64 or 128 rows (draft, query head) of one (sequence, KV
-// head) and a share of its tokens - the first parts exact ones, the others
-// compressed ones, by the sequence's own lengths - in tiles of 128:
+// head) and a share of its tokens - the first parts compressed ones, the others
+// exact ones, by the sequence's own lengths - in tiles of 128:
 //   S^T [128 tokens x rows]  = K^ Q^T      A = key tile, B = queries
 //   O^T [128 coords x rows] += V^T P       A = value tile (token-major), B = P
 // Tokens are on the accumulator's lanes, so a thread owns a token: its scales
@@ -55,11 +55,11 @@
 // warp instructions and 5 k cycles a tile, 56% of the issue slots.
 // Whole calls (CUDA graph, 8 KV heads, theta = 0.05), with the rate of
 // 4 D operations a row and token:
-//   32 k tokens, 32 query heads: 1 draft 33.7 us (212 GB/s of the layout: three
+//   32 k tokens, 32 query heads: 1 draft 34.0 us (210 GB/s of the layout: three
 //     fifths are the pre-kernels, the first tile and the merge), 16 drafts
-//     44.7 us (194 TFLOP/s), 64 drafts 116.5 us (304 TFLOP/s)
-//   128 k tokens, 64 query heads, 24 drafts: 336 us (308 TFLOP/s)
-//   16 sequences of 32 k tokens, theta = 0.1, 8 drafts: 523 us (483 GB/s)
+//     45.4 us (191 TFLOP/s), 64 drafts 116.4 us (304 TFLOP/s)
+//   128 k tokens, 64 query heads, 24 drafts: 301 us (344 TFLOP/s)
+//   16 sequences of 32 k tokens, theta = 0.1, 8 drafts: 474 us (533 GB/s)
 // Anchor rows by four-row TMA gathers were no faster than 16-byte copies (60.4
 // us against 59.8 on 16 drafts then: about 100 cycles of issue a gather);
 // finding the residuals' levels before the rows have landed was slower (36.5 ->
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
   extern __shared__ __align__(1024) unsigned char raw[];
   Sm<NC>& sm = *reinterpret_cast<Sm<NC>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int part = blockIdx.x, blk = blockIdx.y, bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
+  const int blk = blockIdx.x, bh = blockIdx.y, part = blockIdx.z, b = bh / a.H, h = bh % a.H;
   const int64_t unit = (int64_t)bh * a.n_blk + blk;
   float* ml = a.ml + (unit * a.parts + part) * NC * 2;
   const int n_new = tree_new(a, b), rows = n_new * a.G;
@@ -777,14 +777,14 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     asm volatile("griddepcontrol.wait;" ::: "memory");   // this kernel is over after those before it
     return;
   }
-  // this part's tiles: the first parts take the exact tokens, the others the compressed
-  const int lay = a.comp ? tree_layout(a, b) : 0, len = tree_len(a, b), tail_parts = tree_tail_parts(a, len, n_new);
-  const bool tail = part < tail_parts;
+  // this part's tiles: the first parts take the compressed tokens, the others the exact
+  const int lay = a.comp ? tree_layout(a, b) : 0, len = tree_len(a, b), prefix_parts = a.parts - tree_tail_parts(a, len, n_new);
+  const bool tail = part >= prefix_parts;
   const bool out_of_range = lay < 0 || len < 0;
   int tile0, n;
   {
     const int tiles = tail ? (max(len, 0) + n_new + kTT - 1) / kTT : a.n_tiles;
-    const int s = tail ? part : part - tail_parts, of = tail ? tail_parts : a.parts - tail_parts;
+    const int s = tail ? part - prefix_parts : part, of = tail ? a.parts - prefix_parts : prefix_parts;
     tile0 = (int)((int64_t)tiles * s / of);
     n = (int)((int64_t)tiles * (s + 1) / of) - tile0;
   }
@@ -1134,7 +1134,7 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
   int st = ANCHORKV_OK;
   if (a.comp) st = launch_dependent(tree_meta_kernel, dim3((a.n_tiles + 7) / 8, 2 * a.H, a.batch), 256, 0, s, a);
   if (st) return st;
-  st = launch_dependent(tree_tc_kernel<NC>, dim3(a.parts, a.n_blk, a.batch * a.H), Shape<NC>::kThreads, smem_bytes<NC>(), s, a);
+  st = launch_dependent(tree_tc_kernel<NC>, dim3(a.n_blk, a.batch * a.H, a.parts), Shape<NC>::kThreads, smem_bytes<NC>(), s, a);
   if (st) return st;
   return launch_tree_merge<__nv_bfloat16>(a, NC, s);
 }
@@ -1143,45 +1143,61 @@ int launch_nc(const TreeArgs& a, cudaStream_t s) {
 
 int64_t tree_meta_bytes() { return (int64_t)sizeof(Meta); }
 
+// Time of the longest run of CTAs on an SM, in tiles, for units that divide
+// pre + tail tiles over `parts` as tree_tail_parts does.  A CTA costs kFixed
+// tiles beside its own (set-up, first references, outputs), and one of exact
+// tokens, whose rows come from HBM and are scaled on their way, two a tile and
+// two for the first rows' latency.  Parts
+// of exact tokens start last and fill what the others leave.
+static int64_t run_length(int units, int parts, int pre, int tail) {
+  constexpr int kFixed = 6, kSms = 148;
+  const int t = pre ? std::max(1, std::min((int)(((int64_t)tail * parts + pre + tail - 1) / (pre + tail)), parts - 1)) : parts;
+  int a = pre ? (pre + parts - t - 1) / (parts - t) + kFixed : 0, b = 2 * ((tail + t - 1) / t + 1) + kFixed;
+  int n_a = units * (parts - t), n_b = units * t;
+  if (a < b) {
+    std::swap(a, b);
+    std::swap(n_a, n_b);
+  }
+  const int rounds = (n_a + kSms - 1) / kSms;
+  const int64_t fill = b ? (int64_t)(rounds * kSms - n_a) * (a / b) : n_b;
+  return (int64_t)rounds * a + (n_b > fill ? (n_b - fill + kSms - 1) / kSms * b : 0);
+}
+
 void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
-  // One CTA an SM.  A CTA costs about kFixed tiles beside its own (set-up,
-  // first references, outputs) and a tile of 16, 32, 64 or 128 rows the times
-  // below (in tenths of a microsecond, measured over 32 k and 128 k tokens), so
-  // the block and the split are those whose longest run of CTAs on an SM is
-  // shortest.  Larger blocks rebuild each tile for more rows; smaller ones leave
-  // less of a block empty and spread over more SMs.  Measured (8 KV heads, us):
+  // One CTA an SM.  A tile of 16, 32, 64 or 128 rows takes the times below (in
+  // tenths of a microsecond, measured over 32 k and 128 k tokens), so the block
+  // and the parts are those whose longest run of CTAs on an SM is shortest, for
+  // page tables between empty and full.  Larger blocks rebuild each tile for more
+  // rows; smaller ones leave less of a block empty and spread over more SMs.
+  // Measured (8 KV heads, us; each at its own best parts):
   //   rows a head, block of  16     32     64    128
-  //   24,  32 k tokens      51.6   39.1
-  //   64,  32 k             93.6   60.5   45.1
-  //   128, 32 k            178    112     72.3   70.4
-  //   256, 32 k            344    215    135    117
-  //   192, 128 k           873    540    337    389
-  //   32,  16 x 32 k       809    529    688
-  //   64,  16 x 32 k      1507    963    703
-  constexpr int64_t kFixed = 6;
-  constexpr int kRows[4] = {16, 32, 64, 128}, kTime[4] = {12, 14, 17, 29};
+  //   24,  32 k tokens      51.0   39.5
+  //   64,  32 k             85.3   60.9   45.4
+  //   128, 32 k            151    102     72.0   70.0
+  //   256, 32 k            286    187    125    116
+  //   192, 128 k           748    468    301    345
+  //   32,  16 x 32 k       754    474    629
+  //   64,  16 x 32 k      1397    891    639
+  constexpr int kRows[4] = {16, 32, 64, 128}, kTime[4] = {12, 14, 17, 29}, kSms = 148;
   const int pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (int)((tp->cap + tp->T + kTT - 1) / kTT);
   int64_t best = INT64_MAX;
   for (int k = 0; k < 4; ++k) {
     const int n_blk = (tp->rows + kRows[k] - 1) / kRows[k], units = tp->batch * pl.H * n_blk;
-    // as many CTAs a unit as fill a whole number of waves
-    const int first = std::max(1, (units * (prefix ? 2 : 1) + 147) / 148);
-    for (int waves = first; waves < first + 16; ++waves) {
-      const int parts = std::max(prefix ? 2 : 1, std::min(148 * waves / units, pre + tail));
-      int per = (tail + parts - 1) / parts;
-      if (prefix) {                        // as tree_tail_parts divides them
-        const int t = std::max(1, std::min((int)(((int64_t)tail * parts + pre + tail - 1) / (pre + tail)), parts - 1));
-        per = std::max((pre + parts - t - 1) / (parts - t), (tail + t - 1) / t);
+    // as many parts of compressed tokens (with and without one of exact tokens
+    // beside them) as fill a whole number of rounds
+    const int first = std::max(1, (units + kSms - 1) / kSms);
+    for (int rounds = first; rounds < first + 12; ++rounds)
+      for (int more = prefix; more >= 0; --more) {
+        const int parts = std::max(prefix ? 2 : 1, std::min(kSms * rounds / units + more, pre + tail));
+        const int64_t cost = (run_length(units, parts, pre, tail) + run_length(units, parts, pre, 1)) * kTime[k];
+        if (cost < best) {
+          best = cost;
+          tp->RB = kRows[k];
+          tp->n_blk = n_blk;
+          tp->parts = parts;
+          tp->tail_parts = prefix ? 0 : parts;
+        }
       }
-      const int64_t cost = ((int64_t)units * parts + 147) / 148 * (per + kFixed) * kTime[k];
-      if (cost < best) {
-        best = cost;
-        tp->RB = kRows[k];
-        tp->n_blk = n_blk;
-        tp->parts = parts;
-        tp->tail_parts = prefix ? 0 : parts;
-      }
-    }
   }
 }
 
