@@ -83,11 +83,24 @@ constexpr int kSt = 2;                    // stages of the key and value rings
 constexpr int kTileBytes = kTT * kD * 2;
 constexpr int kHalf = kTileBytes / 2;     // 64 coordinates of every row
 constexpr float kLog2e = 1.4426950408889634f;
-// A new reference puts the largest |w p| between 2^-6 and 2^-5: 20 bits below
-// the limit for later tiles, and what fp16 rounds away below 2^-14 is at most
-// 2^-19 of the largest contribution each.
+// P is fp16: w p over its reference, between 2^-24 (the smallest step) and 2^15.
+// A token's rounding is at most 2^-25, but of n tokens behind one that takes
+// nearly all (a prompt's first, as a rule) all may round the same way, and the
+// sum of p keeps what the outputs lose.  So a new reference puts the largest
+// |w p| at 2^-t / 2 or above, t = 13 - log2 n for the n tokens of the part: the
+// loss of all of them, n 2^-25, is then at most 2^-11 of that largest
+// contribution, one rounding of an operand.  What is left up to 2^15 is
+// headroom: a tile that passes it pays for new references, so it goes with the
+// part (17 bits for 2 k tokens, 13 for 32 k, 8 for 2^20).  Against 20 bits for
+// every part, which lost 1.6% of the output behind a first token 14 nats above
+// 32 k others and 5% of 128 k (graph, us; q scaled by 1 and 8): one draft 34.4,
+// 42.6 -> 34.8, 42.6; 64 drafts 116.4, 192 -> 122.5, 199; batch 16 475, 535 ->
+// 478, 552.  With 2^8 for every part: 38.9, 46.5; 156, 216; 500, 577.
 constexpr float kPLimit = 32768.f;        // fp16 holds 65504
-constexpr float kPTarget = 5.f;
+constexpr int kPBits = 13, kPMost = 5;    // t, at most
+__device__ __forceinline__ float p_target(int tiles) {
+  return (float)min(kPMost, kPBits - 7 - (32 - __clz(tiles - 1)));   // 2^7 tokens a tile
+}
 constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
 constexpr float kRefGap = 120.f;          // the references' largest distance downwards
 
@@ -154,6 +167,7 @@ struct Sm {
   uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[S::kKSl], sv[S::kVSl];   // full: [side][stage]
   uint64_t loaded[2][S::kMetaSl], coded[2][S::kCodeSl];     // token tables, codes
   uint32_t tmem;
+  float target;                           // t of new references
   int err, bad, rep;
 };
 template <int NC>
@@ -735,7 +749,7 @@ __device__ __noinline__ void new_references(M& sm, const TreeArgs& a, uint32_t s
     const float m2 = unordered(max(max(r[1][0][tok], r[1][1][tok]), max(r[1][2][tok], r[1][3][tok])));
     const float l_old = -sm.nm[par][c], p_old = sm.mp[par][c];
     const float l_new = fmaxf(l_old, ceilf(m1));
-    float p_new = fmaxf(p_old, ceilf(m2) + kPTarget);
+    float p_new = fmaxf(p_old, ceilf(m2) + sm.target);
     if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
     sm.fl[par][c] = l_old > -INFINITY ? pow2(l_old - l_new) : 0.f;
     sm.nm[par][c] = -l_new;
@@ -819,6 +833,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       tc::mbar_init(&sm.pfull[lane], 4 * CG);
     }
     if (lane == 0) {
+      sm.target = p_target(n);
       sm.err = 0;
       sm.bad = 0;
     }

@@ -292,6 +292,89 @@ def test_logits_and_values_that_keep_growing(dtype, T, up):
     assert ((got - want).norm(dim=3) <= tol).all()
 
 
+def sink_tolerance(q, K, V, Kn, Vn, u, n, half):
+    """(outputs, tolerance) of rows q over tokens K, V, with a logit's error counted token by token.
+
+    With |delta_t| <= E_t = (n u + D 2^-24) |q| Kn_t / sqrt(D) the error of the probabilities moves the output by at
+    most e^max(E) sum_t p_t (e^E_t - 1) |V_t - o|, and rounding p_t w_t and a value's row by (n + 1) u p_t Vn_t each;
+    the output's own step is half of ||o||.  No term leaves room for tokens that are dropped."""
+    s = q @ K.T / math.sqrt(D)
+    pr = torch.softmax(s, 1)
+    o = pr @ V
+    E = (n * u + D * 2.0 ** -24) * q.norm(dim=1)[:, None] * Kn / math.sqrt(D)
+    far = torch.cdist(o, V)
+    tol = E.amax(1).exp() * (pr * torch.expm1(E) * far).sum(1) + (n + 1) * u * (pr @ Vn) + half * o.norm(dim=1)
+    return o, tol
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("tokens,gap,spread,size", [
+    (32768, 14.0, 0.3, 1.0), (32768, 16.0, 0.3, 0.1), (32768, 14.0, 1.0, 1.0), (131072, 14.0, 0.3, 1.0),
+    (131072, 16.0, 1.0, 0.1), (131072, 17.0, 0.1, 0.3)])
+def test_sink_before_many_small_tokens(dtype, tokens, gap, spread, size):
+    """The first token takes nearly all, tens of thousands of small ones behind it together a few percent, all in one
+    part (as many sequences as fill the SMs): none of what the small ones add is lost.  Exact tokens of bf16 caches
+    are fp16 operands without a rounding (n = 0)."""
+    H, B, page, g = 4, 37, 128, torch.Generator().manual_seed(5)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    u = torch.randn(H, D, generator=g)
+    u /= u.norm(dim=1, keepdim=True)
+    q = (8 * (u + 0.02 * torch.randn(B, H, D, generator=g))).to(dt)
+    along = spread * math.sqrt(D) / 8 * torch.randn(H, tokens, 1, generator=g)
+    K = along * u[:, None] + 0.01 * torch.randn(H, tokens, D, generator=g)
+    K[:, 0] = gap * math.sqrt(D) / 8 * u
+    V = 1 + 0.3 * torch.randn(H, tokens, D, generator=g)
+    V[:, 0] = size * torch.randn(H, D, generator=g)
+    K, V = K.to(dt), V.to(dt)
+    spec = api.PageSpec(n_pages=tokens // page, page_size=page, n_slots=B, max_pages=tokens // page, n_kv_heads=H, dtype=dtype)
+    state = torch.zeros(spec.state_numel, dtype=torch.int32)
+    v = api.pages_view(spec, state)
+    v["len"][:] = tokens
+    v["table"][:] = torch.arange(spec.n_pages)
+    p = api.AnchorKVParams(n_tokens=1024, n_kv_heads=H, n_q_heads=H, dtype=dtype)
+    pools = [x.reshape(H, -1, page, D).transpose(0, 1).contiguous().cuda() for x in (K, V)]
+    Kn, Vn = (torch.randn(B, 1, H, D, generator=g).to(dt) for _ in range(2))
+    mask = torch.zeros(B, 1, dtype=torch.int64)                              # the draft sees the tail alone
+    got = api.tree_attn(p, None, q[:, None].cuda(), Kn.cuda(), Vn.cuda(), mask=mask.cuda(), pages=spec, state=state.cuda(),
+                        K_pages=pools[0], V_pages=pools[1])[:, 0].cpu().double()
+    unit, n, half = (2.0 ** -24, 128, 2.0 ** -24) if dtype == "fp32" else (2.0 ** -11, 0, 2.0 ** -8)
+    for h in range(H):
+        k, x = K[h].double(), V[h].double()
+        want, tol = sink_tolerance(q[:, h].double(), k, x, k.norm(dim=1), x.norm(dim=1), unit, n, half)
+        off = (got[:, h] - want).norm(dim=1)
+        assert (off <= tol).all(), (off / tol).max()
+
+
+@gpu
+def test_sink_of_a_compressed_prompt():
+    """The same behind a compressed prompt, whose rows are rounded like all others."""
+    H, B, N, g = 4, 37, 32768, torch.Generator().manual_seed(6)
+    u = torch.randn(H, D, generator=g)
+    u /= u.norm(dim=1, keepdim=True)
+    q = (8 * (u + 0.02 * torch.randn(B, H, D, generator=g))).bfloat16()
+    K = 0.4 * torch.randn(H, N, 1, generator=g) * u[:, None] + 0.1 * torch.randn(H, N, D, generator=g)
+    K[:, 0] = 14 * math.sqrt(D) / 8 * u
+    V = 1 + 0.3 * torch.randn(H, N, D, generator=g)
+    V[:, 0] = torch.randn(H, D, generator=g)
+    p = api.AnchorKVParams(n_tokens=N, n_kv_heads=H, n_q_heads=H, theta=0.05)
+    po = O.Params(n_tokens=N, n_kv_heads=H, n_q_heads=H, theta=0.05, dtype="bf16")
+    comp, ws = api.compress(p, K.bfloat16().cuda(), V.bfloat16().cuda(), q[:32].transpose(0, 1).contiguous().cuda())
+    assert api.read_status(ws)[0] == 0
+    parts = O.unpack_layout(comp.cpu().numpy(), po)
+    full, bare = O.reconstruct(parts, po), O.reconstruct(dict(parts, codes=np.zeros((0, D), np.uint8)), po)
+    dense = [(torch.tensor(f), torch.tensor(np.linalg.norm(a, axis=-1) + np.linalg.norm(f - a, axis=-1)))
+             for f, a in zip(full, bare)]
+    Kn, Vn = (torch.randn(B, 1, H, D, generator=g).bfloat16() for _ in range(2))
+    got = api.tree_attn(p, comp, q[:, None].cuda(), Kn.cuda(), Vn.cuda(), mask=torch.zeros(B, 1, dtype=torch.int64).cuda(),
+                        layout_of=torch.zeros(B, dtype=torch.int32).cuda())[:, 0].cpu().double()
+    for h in range(H):
+        (k, kn), (x, xn) = ((d[h].double(), m[h].double()) for d, m in dense)
+        want, tol = sink_tolerance(q[:, h].double(), k, x, kn, xn, 2.0 ** -11, 3, 2.0 ** -8)
+        off = (got[:, h] - want).norm(dim=1)
+        assert (off <= tol).all(), (off / tol).max()
+
+
 @gpu
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("gamma", [0.0, 6e-8, 1e-5, 1e-3, -1.0, "by token"])
