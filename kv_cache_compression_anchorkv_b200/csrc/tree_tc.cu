@@ -102,7 +102,11 @@ __device__ __forceinline__ float p_target(int tiles) {
   return (float)min(kPMost, kPBits - 7 - (32 - __clz(tiles - 1)));   // 2^7 tokens a tile
 }
 constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
-constexpr float kRefGap = 120.f;          // the references' largest distance downwards
+constexpr float kRefGap = 120.f;          // the references' largest distance, either way
+// A part's sum is handed to the merge between 2^-12 and 2^-11, and its outputs in
+// the same unit: 2^11 parts of the largest finite values add up to a finite
+// number, and a bf16 output keeps its bits down to the smallest normal one.
+constexpr int kSumBits = 11;
 
 // What a tile of one side needs beside rows and codes, written by the
 // pre-kernel: per token its scale and its anchor slot; per residual record the
@@ -750,7 +754,7 @@ __device__ __noinline__ void new_references(M& sm, const TreeArgs& a, uint32_t s
     const float l_old = -sm.nm[par][c], p_old = sm.mp[par][c];
     const float l_new = fmaxf(l_old, ceilf(m1));
     float p_new = fmaxf(p_old, ceilf(m2) + sm.target);
-    if (l_new > -INFINITY) p_new = fmaxf(p_new, l_new - kRefGap);
+    if (l_new > -INFINITY) p_new = fminf(fmaxf(p_new, l_new - kRefGap), l_new + kRefGap);   // cw is a normal number
     sm.fl[par][c] = l_old > -INFINITY ? pow2(l_old - l_new) : 0.f;
     sm.nm[par][c] = -l_new;
     sm.mp[par][c] = p_new;
@@ -1088,13 +1092,21 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
 #pragma unroll
       for (int k = 0; k < PG; ++k) {
         const float sum = sm.lsum[k][0][c] + sm.lsum[k][1][c] + sm.lsum[k][2][c] + sm.lsum[k][3][c];
+        l += sm.nm[k][c] < INFINITY ? sum * pow2(-sm.nm[k][c] - m) : sum;   // a sum without a reference is zero, or NaN
+      }
+      // the unit: a power of two, so that nothing is rounded
+      const int shift = l > 0.f && l < INFINITY ? (__float_as_int(l) >> 23) - 126 + kSumBits : 0;
+#pragma unroll
+      for (int k = 0; k < PG; ++k) {
+        // two factors: one alone can be out of fp32's range, above it for values near their largest
+        const float d = sm.mp[k][c] - m - (float)shift, half = floorf(0.5f * d);
         const bool has = sm.nm[k][c] < INFINITY;
-        l += has ? sum * pow2(-sm.nm[k][c] - m) : sum;             // a sum without a reference is zero, or NaN
-        fo[k * 32 + tok] = has ? pow2(sm.mp[k][c] - m) : 0.f;
+        fo[k * 32 + tok] = has ? pow2(half) : 0.f;
+        fo[64 + k * 32 + tok] = pow2(d - half);
       }
       if (par == 0) {
-        ml[2 * c] = nan ? 0.f : m;
-        ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : l;
+        ml[2 * c] = nan ? 0.f : m + (float)shift;
+        ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : l * pow2((float)-shift);
       }
     }
     if (n > 1) wait_b(sm, &sm.pv[(n - 2) & 1], ((n - 2) >> 1) & 1, a);
@@ -1110,8 +1122,8 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         // a parity without a reference has nothing (and, without a tile, no number) there
-        float acc = fo[x + y] != 0.f ? __uint_as_float(v[0][y]) * fo[x + y] : 0.f;
-        if (PG == 2 && fo[32 + x + y] != 0.f) acc = fmaf(__uint_as_float(v[PG - 1][y]), fo[32 + x + y], acc);
+        float acc = fo[x + y] != 0.f ? __uint_as_float(v[0][y]) * fo[x + y] * fo[64 + x + y] : 0.f;
+        if (PG == 2 && fo[32 + x + y] != 0.f) acc = fmaf(__uint_as_float(v[PG - 1][y]) * fo[32 + x + y], fo[96 + x + y], acc);
         o[(x + y) * kD] = acc;
       }
     }

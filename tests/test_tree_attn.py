@@ -292,6 +292,26 @@ def test_logits_and_values_that_keep_growing(dtype, T, up):
     assert ((got - want).norm(dim=3) <= tol).all()
 
 
+@gpu
+@pytest.mark.parametrize("T", [1, 3, 24])
+@pytest.mark.parametrize("scale", [2.0 ** -122, 2.0 ** -110, 2.0 ** 110, 2.0 ** 120, 2.0 ** 123, 3.3e38])
+def test_finite_values_near_the_ends_of_their_type(scale, T):
+    """bf16 values of drafts and tail close to the largest and to the smallest normal number: the outputs are averages
+    of them, so they are finite too; below the normal range a step of the output is 2^-133."""
+    g = torch.Generator().manual_seed(11)
+    pr = Problem(T=T, lens=[900, 7], page=64, prefix=False)
+    sign = lambda x: torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0)                # noqa: E731
+    span = lambda x: (0.5 + 0.5 * torch.rand(x.shape, generator=g)) * scale                        # noqa: E731
+    for signs in (sign, lambda x: 1.0):
+        pr.Vp, pr.Vn = ((signs(x) * span(x)).to(torch.bfloat16) for x in (pr.Vp, pr.Vn))
+        assert torch.isfinite(pr.Vp).all() and torch.isfinite(pr.Vn).all()
+        got = pr.call().cpu().double()
+        want, tol = pr.expect()
+        assert torch.isfinite(got).all()
+        off = (got - want).norm(dim=3)
+        assert (off <= tol + 2.0 ** -134 * math.sqrt(D)).all(), (off / tol).max()
+
+
 def sink_tolerance(q, K, V, Kn, Vn, u, n, half):
     """(outputs, tolerance) of rows q over tokens K, V, with a logit's error counted token by token.
 
