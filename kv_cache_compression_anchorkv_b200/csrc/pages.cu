@@ -627,8 +627,9 @@ int anchorkv_pages_fork(const anchorkv_pages* pg, const int32_t* state_in, int32
   if (st) return st;
   a.parents = parents;
   cudaStream_t s = (cudaStream_t)stream;
+  // 48 KB without an attribute, the kernel's own arrays among them
   const int smem = 4 * a.S * 4;
-  if (smem > 48 * 1024 &&
+  if (smem > 32 * 1024 &&
       cudaFuncSetAttribute(fork_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return ANCHORKV_ECUDA;
   stage_begin(kStPages, s);

@@ -182,6 +182,24 @@ def test_many_slots_and_wide_tables():
     m.same(state, Kg, Vg)
 
 
+@gpu
+@pytest.mark.parametrize("slots", [2047, 2049, 3063, 3064, 3071, 3073, 4096])
+def test_fork_of_as_many_slots_as_there_may_be(slots):
+    """Shared memory goes with the slots: on both sides of the size that needs an attribute, and the most."""
+    spec = api.PageSpec(n_pages=slots, page_size=16, n_slots=slots, max_pages=2, n_layers=1, n_kv_heads=1)
+    g, K, V = make(spec)
+    m, Kg, Vg = Model(spec, K, V), K.cuda(), V.cuda()
+    state = api.pages_init(spec)
+    n = torch.randint(0, 17, (slots,), generator=g).tolist()
+    Kn, Vn = drafts(spec, slots, 16, g)
+    m.commit(Kn, Vn, n, None)
+    api.pages_commit(spec, state, Kg, Vg, Kn.cuda(), Vn.cuda(), i32(n))
+    parents = torch.randint(-1, slots, (slots,), generator=g).tolist()
+    m.fork(parents)
+    api.pages_fork(spec, state, Kg, Vg, i32(parents))
+    m.same(state, Kg, Vg)
+
+
 REFUSED = [
     ("free", 1), ("table", 2), ("count", 3), ("count_below", 3), ("path", 3), ("parent", 3), ("parent_below", 3),
     ("len", 3), ("entry", 3), ("shared_tail", 3), ("no_page_to_fork", 1),
