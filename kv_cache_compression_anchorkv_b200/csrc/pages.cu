@@ -100,6 +100,15 @@ __device__ void refuse(const PgArgs& a, int code) {
   }
 }
 
+// The code that threads have raised in shared memory, the same for all of them:
+// none raises it again before all have read it.
+__device__ __forceinline__ int refused(const int* bad) {
+  __syncthreads();
+  const int code = *(const volatile int*)bad;
+  __syncthreads();
+  return code;
+}
+
 __device__ __forceinline__ void header_out(const PgArgs& a, int status, int n_free, int items) {
   if (threadIdx.x < kPageHeader) a.out[threadIdx.x] = threadIdx.x == 0 ? status : threadIdx.x == 1 ? n_free : 0;
   if (threadIdx.x == 0) a.ws[0] = items;
@@ -161,20 +170,18 @@ __global__ void __launch_bounds__(kMetaThreads) commit_state_kernel(PgArgs a) {
     block_scan(need, tmp, &total);
     need_all += total;
   }
-  if (need_all > n_free && !bad) {
-    __syncthreads();
-    refuse(a, kPgNoFree);
+  const int why_not = refused(&bad);
+  if (why_not || need_all > n_free) {
+    refuse(a, why_not ? why_not : kPgNoFree);
     return;
   }
   // the ids that will be handed out
-  if (!bad)
-    for (int i = tid; i < need_all; i += kMetaThreads) {
-      const int id = a.in[kPageHeader + n_free - 1 - i];
-      if (id < 0 || id >= a.n_pages) atomicMax(&bad, kPgRange);
-    }
-  __syncthreads();
-  if (bad) {
-    refuse(a, bad);
+  for (int i = tid; i < need_all; i += kMetaThreads) {
+    const int id = a.in[kPageHeader + n_free - 1 - i];
+    if (id < 0 || id >= a.n_pages) atomicMax(&bad, kPgRange);
+  }
+  if (refused(&bad)) {
+    refuse(a, kPgRange);
     return;
   }
   if (a.out != a.in) {
@@ -276,9 +283,10 @@ __global__ void __launch_bounds__(kMetaThreads) fork_state_kernel(PgArgs a) {
       atomicAdd(&children[p], 1);
     }
   }
-  __syncthreads();
-  if (bad) {
-    refuse(a, bad);
+  // `bad` is raised again below: every thread reads it before any goes on, so
+  // that all take the same branch
+  if (refused(&bad)) {
+    refuse(a, kPgRange);
     return;
   }
   // holders of every page afterwards, the new copies aside (whole numbers:
@@ -311,10 +319,9 @@ __global__ void __launch_bounds__(kMetaThreads) fork_state_kernel(PgArgs a) {
     const int id = a.in[kPageHeader + i];
     if (id < 0 || id >= a.n_pages) atomicMax(&bad, kPgRange);
   }
-  __syncthreads();
-  const int have = n_free + n_freed;
-  if (bad || have > a.n_pages || n_copy > have) {
-    refuse(a, bad || have > a.n_pages ? kPgRange : kPgNoFree);
+  const int why_not = refused(&bad), have = n_free + n_freed;
+  if (why_not || have > a.n_pages || n_copy > have) {
+    refuse(a, why_not || have > a.n_pages ? kPgRange : kPgNoFree);
     return;
   }
   // the old table, where the new one overwrites it
@@ -412,8 +419,8 @@ __global__ void __launch_bounds__(kMetaThreads) compact_state_kernel(PgArgs a) {
     const int i = i0 + tid;
     n += __syncthreads_count(i < a.n_pages && refs[i] > 0);
   }
-  if (bad) {
-    refuse(a, bad);
+  if (refused(&bad)) {
+    refuse(a, kPgRange);
     return;
   }
   // i-th used page at n or behind, i-th free page below n: as many of the one

@@ -273,6 +273,39 @@ def test_refused_operations_change_nothing(what, code, in_place):
 
 
 @gpu
+@pytest.mark.parametrize("in_place", [True, False])
+def test_bad_entries_seen_by_any_warp_are_refused_alike(in_place):
+    """A table entry out of range that one warp of the state kernel meets early or late, many times over: the whole
+    block refuses, and the scratch of a refused call serves the next one."""
+    spec = api.PageSpec(n_pages=200, page_size=16, n_slots=100, max_pages=3, n_layers=1, n_kv_heads=1)
+    g, K, V = make(spec)
+    m, Kg, Vg = Model(spec, K, V), K.cuda(), V.cuda()
+    state = api.pages_init(spec)
+    Kn, Vn = drafts(spec, spec.n_slots, 30, g)
+    n = torch.randint(0, 31, (spec.n_slots,), generator=g).tolist()
+    n[0] = n[31] = n[32] = n[99] = 20
+    m.commit(Kn, Vn, n, None)
+    api.pages_commit(spec, state, Kg, Vg, Kn.cuda(), Vn.cuda(), i32(n))
+    ws = torch.empty(api.pages_workspace_bytes(spec), dtype=torch.uint8, device="cuda")
+    parents = i32(list(range(spec.n_slots)))
+    for slots in ([0], [31], [32], [99], [0, 99], [31, 32]):
+        broken = state.clone()
+        for s in slots:
+            api.pages_view(spec, broken)["table"][s, 0] = spec.n_pages
+        want = broken.clone()
+        want[0] = 3
+        for op in (lambda st, out: api.pages_fork(spec, st, Kg, Vg, parents, state_out=out, workspace=ws),
+                   lambda st, out: api.pages_compact(spec, st, Kg, Vg, state_out=out, workspace=ws)):
+            for _ in range(25):
+                st = broken.clone()
+                assert torch.equal(op(st, None if in_place else torch.full_like(st, -7)), want)
+    m.same(state, Kg, Vg)
+    m.fork(list(range(spec.n_slots)))
+    api.pages_fork(spec, state, Kg, Vg, parents, workspace=ws)
+    m.same(state, Kg, Vg)
+
+
+@gpu
 def test_freed_pages_serve_the_forks_of_the_same_call():
     spec = api.PageSpec(n_pages=4, page_size=16, n_slots=3, max_pages=3, n_layers=2, n_kv_heads=2)
     g, K, V = make(spec)
