@@ -346,7 +346,8 @@ int anchorkv_decode_attn_noalloc(const anchorkv_params* p, const void* compresse
  * keys and values, and take effect whole or not at all: where the device
  * finds that an operation cannot be done, the status word of state_out keeps
  * the first code (1: too few free pages, 2: a page table is full, 3: an
- * argument or a table entry out of its range) and nothing else changes.  The
+ * argument or an entry of the state out of its range, or a count that the
+ * tables or the free list contradict) and nothing else changes.  The
  * word stays set until anchorkv_pages_init; anchorkv_read_device_status reads
  * it.  Which pages are handed out depends on the state alone.
  */

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kMetaThreads) commit_state_kernel(PgArgs a) {
   // the ids that will be handed out
   for (int i = tid; i < need_all; i += kMetaThreads) {
     const int id = a.in[kPageHeader + n_free - 1 - i];
-    if (id < 0 || id >= a.n_pages) atomicMax(&bad, kPgRange);
+    if (id < 0 || id >= a.n_pages || a.in[o_refs(a) + id] != 0) atomicMax(&bad, kPgRange);
   }
   if (refused(&bad)) {
     refuse(a, kPgRange);
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kMetaThreads) fork_state_kernel(PgArgs a) {
     const int full = len_old[p] / a.P, used = (len_old[p] + a.P - 1) / a.P, kids = children[p];
     for (int c = lane; c < used; c += 32) {
       const int pg = table_in[(int64_t)p * a.maxp + c];
-      if (pg < 0 || pg >= a.n_pages) atomicMax(&bad, kPgRange);
+      // a page that nobody holds could be handed out below
+      if (pg < 0 || pg >= a.n_pages || a.in[o_refs(a) + pg] <= 0) atomicMax(&bad, kPgRange);
       else if (kids) atomicAdd(&count[pg], c < full ? kids : 1);
     }
   }
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kMetaThreads) fork_state_kernel(PgArgs a) {
   }
   for (int i = tid; i < n_free; i += kMetaThreads) {
     const int id = a.in[kPageHeader + i];
-    if (id < 0 || id >= a.n_pages) atomicMax(&bad, kPgRange);
+    if (id < 0 || id >= a.n_pages || a.in[o_refs(a) + id] != 0) atomicMax(&bad, kPgRange);
   }
   const int why_not = refused(&bad), have = n_free + n_freed;
   if (why_not || have > a.n_pages || n_copy > have) {

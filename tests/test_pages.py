@@ -306,6 +306,36 @@ def test_bad_entries_seen_by_any_warp_are_refused_alike(in_place):
 
 
 @gpu
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("what", ["held page without a holder", "last page without a holder", "free page with a holder"])
+def test_counts_that_contradict_the_state_are_refused(what, in_place):
+    """A page in use that counts as nobody's, or a free one that counts as somebody's: it could be handed out over
+    rows that are still read, so nothing is done with such a state."""
+    spec = api.PageSpec(n_pages=8, page_size=16, n_slots=3, max_pages=3, n_layers=2, n_kv_heads=2)
+    g, K, V = make(spec)
+    m, Kg, Vg = Model(spec, K, V), K.cuda(), V.cuda()
+    state = api.pages_init(spec)
+    Kn, Vn = drafts(spec, 3, 64, g)
+    m.commit(Kn, Vn, [20, 33, 5], None)
+    api.pages_commit(spec, state, Kg, Vg, Kn.cuda(), Vn.cuda(), i32([20, 33, 5]))
+    view = api.pages_view(spec, state)
+    if what == "free page with a holder":
+        view["refs"][m.free[-1]] = 1
+        ops = [lambda st, out: api.pages_commit(spec, st, Kg, Vg, Kn.cuda(), Vn.cuda(), i32([0, 0, 12]), state_out=out)]
+    else:
+        view["refs"][m.table[1][0 if what == "held page without a holder" else -1]] = 0
+        ops = [lambda st, out: api.pages_compact(spec, st, Kg, Vg, state_out=out)]
+    ops.append(lambda st, out: api.pages_fork(spec, st, Kg, Vg, i32([0, 1, 1]), state_out=out))
+    want, Kb, Vb = state.clone(), Kg.clone(), Vg.clone()
+    want[0] = 3
+    for op in ops:
+        st = state.clone()
+        got = op(st, None if in_place else torch.full_like(st, -7))
+        assert torch.equal(got, want)
+        assert torch.equal(Kg, Kb) and torch.equal(Vg, Vb)
+
+
+@gpu
 def test_freed_pages_serve_the_forks_of_the_same_call():
     spec = api.PageSpec(n_pages=4, page_size=16, n_slots=3, max_pages=3, n_layers=2, n_kv_heads=2)
     g, K, V = make(spec)
