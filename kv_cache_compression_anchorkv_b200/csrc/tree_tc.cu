@@ -170,6 +170,10 @@ struct Sm {
   unsigned char colt[kRows];              // draft of each row
   uint64_t full[2][2], kempty[2], pv[2], sfull[2], sempty[2], pfull[2], sk[S::kKSl], sv[S::kVSl];   // full: [side][stage]
   uint64_t loaded[2][S::kMetaSl], coded[2][S::kCodeSl];     // token tables, codes
+  // their places are free: a barrier each.  kempty and pv, which the tile after
+  // next uses again, would not do: it may be done before a late loader looks, and
+  // the parity would say "not yet" until a tile that waits for the loader.
+  uint64_t freed[2][S::kMetaSl];
   uint32_t tmem;
   float target;                           // t of new references
   int err, bad, rep;
@@ -487,7 +491,7 @@ __device__ void load_side(const TreeArgs& a, M& sm, int side, int n, const uint8
   const uint8_t* codes = comp + a.off_codes;
   for (int t = 0; t <= n; ++t) {
     const int before = t - kMetaSl;
-    if (before >= 0) wait_b(sm, side ? &sm.pv[before & 1] : &sm.kempty[before & 1], (before >> 1) & 1, a);
+    if (before >= 0) wait_b(sm, &sm.freed[side][before % kMetaSl], (before / kMetaSl) & 1, a);
     if (t < n) {
       uint64_t* mb = &sm.loaded[side][t % kMetaSl];
       tc::mbar_expect_tx(mb, sizeof(Table));
@@ -826,7 +830,10 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     // arrival a warp
     if (lane < kKSl) tc::mbar_init(&sm.sk[lane], tail ? 4 : 1);
     if (lane < kVSl) tc::mbar_init(&sm.sv[lane], tail ? 4 : 1);
-    if (lane < 2 * S::kMetaSl) tc::mbar_init(&sm.loaded[0][0] + lane, 1);
+    if (lane < 2 * S::kMetaSl) {
+      tc::mbar_init(&sm.loaded[0][0] + lane, 1);
+      tc::mbar_init(&sm.freed[0][0] + lane, 1);
+    }
     if (lane < 2 * S::kCodeSl) tc::mbar_init(&sm.coded[0][0] + lane, 1);
     if (lane < 4) tc::mbar_init(&sm.full[0][0] + lane, 4);
     if (lane < 2) {
@@ -918,7 +925,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     // ---- logits: S^T = K^ Q^T.  After a failed wait the products go on with
     // whatever is there; the outputs become NaN at the end.
     const uint64_t kd = tc::sw128_desc(tc::smem_u32(sm.K)), qd = tc::sw128_desc(tc::smem_u32(sm.Q));
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0, place = 0; i < n; ++i) {
       const int bf = i & 1;
       wait_b(sm, &sm.full[0][bf], (i >> 1) & 1, a);
       if (i >= 2) wait_b(sm, &sm.sempty[bf], ((i >> 1) - 1) & 1, a);
@@ -926,13 +933,18 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       tc::fence_after_sync();
       mma_tile<2, kHalf / 16 - 6, 2, NC * 8 - 6>(tmem + kSCol + bf * NC, kd + bf * (kTileBytes / 16), qd, idesc_f16(128, NC, 0, 0), 0);
       commit_elected(&sm.kempty[bf]);
+      if (!tail) commit_elected(&sm.freed[0][place]);
+      place = place + 1 < S::kMetaSl ? place + 1 : 0;
       commit_elected(&sm.sfull[bf]);
     }
-    tc::mbar_wait(&sm.sfull[(n - 1) & 1], ((n - 1) >> 1) & 1);     // in every case over before the memory is freed
+    // all of it over before the memory is freed, in every case
+    tc::mbar_wait(&sm.sfull[(n - 1) & 1], ((n - 1) >> 1) & 1);
+    tc::mbar_wait(&sm.kempty[(n - 1) & 1], ((n - 1) >> 1) & 1);
+    if (!tail) tc::mbar_wait(&sm.freed[0][(n - 1) % S::kMetaSl], ((n - 1) / S::kMetaSl) & 1);
   } else if (warp == kMma + 1) {
     // ---- outputs: O^T += V^T P
     const uint64_t vd = tc::sw128_mn_desc(tc::smem_u32(sm.V), kHalf), pd = tc::sw128_mn_desc(tc::smem_u32(sm.P), kTT * 128);
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0, place = 0; i < n; ++i) {
       const int bf = i & 1;
       wait_b(sm, &sm.full[1][bf], (i >> 1) & 1, a);
       wait_b(sm, &sm.pfull[bf], (i >> 1) & 1, a);
@@ -940,9 +952,12 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       tc::fence_after_sync();
       mma_tile<128, 128, 128, 128>(tmem + (PG == 2 ? bf * kOCols : 0), vd + bf * (kTileBytes / 16),
                                    pd + (S::kPBuf == 2 ? bf * (S::kPBytes / 16) : 0), idesc_f16(128, kOCols, 1, 1), i >= PG);
+      if (!tail) commit_elected(&sm.freed[1][place]);
       commit_elected(&sm.pv[bf]);
+      place = place + 1 < S::kMetaSl ? place + 1 : 0;
     }
     tc::mbar_wait(&sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1);
+    if (!tail) tc::mbar_wait(&sm.freed[1][(n - 1) % S::kMetaSl], ((n - 1) / S::kMetaSl) & 1);
   } else {
     // ---- softmax: thread = token; a group of four warps has CW of the rows and,
     // where two groups share them, every other tile with references, sums and

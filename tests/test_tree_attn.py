@@ -437,6 +437,27 @@ def test_infinity_in_a_committed_value(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("T", [1, 8, 16, 32])
+@pytest.mark.parametrize("tail", [0, 6000])
+def test_long_parts_of_every_block_size(T, tail):
+    """As many sequences as give every SM one block of 16, 32, 64 or 128 rows with a whole prompt in one part, so that
+    each place of the pipeline is used over and over; 16 replays give the same bits."""
+    H, G, B, N = 4, 4, 37, 8192
+    pr = Problem(H=H, G=G, N=N, B=B, layouts=1, T=T, theta=0.1, lens=[tail] + [0] * (B - 1) if tail else None, page=64)
+    first = pr.call()
+    for _ in range(16):
+        assert torch.equal(pr.call(), first)
+    one = Problem.__new__(Problem)                                        # sequences 0 and 36, by themselves
+    for b in (0, B - 1):
+        one.__dict__.update(pr.__dict__)
+        one.B, one.layout_of, one.lens = 1, pr.layout_of[b:b + 1], pr.lens[b:b + 1]
+        one.q, one.Kn, one.Vn, one.mask = (x[b:b + 1] for x in (pr.q, pr.Kn, pr.Vn, pr.mask))
+        if b:
+            one.pages = None
+        one.check(out=first[b:b + 1])
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_many_beams_of_one_prompt(dtype):
     """More sequences than a warp has lanes, on one layout, with tails of every length."""
