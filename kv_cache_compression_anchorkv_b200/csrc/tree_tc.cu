@@ -1095,7 +1095,11 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       if (lane < 16) sm.lsum[par][wq][c0 + 16 * ch + lane] = l;
     }
     // outputs in units of the sum's reference (of the larger, where two groups
-    // have these rows; each writes half of them)
+    // have these rows; each writes half of them), once all waits of these groups
+    // are over: one that failed makes the rows NaN
+    if (n > 1) wait_b(sm, &sm.pv[(n - 2) & 1], ((n - 2) >> 1) & 1, a);
+    wait_b(sm, &sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, a);
+    tc::fence_after_sync();
     tc::named_bar(8 + grp / PG, 128 * PG);
     const bool nan = *(volatile int*)&sm.err || *(volatile int*)&sm.bad;
     if (nan && tid == 0) latch_error(a.counters, kDevErrBounds);
@@ -1124,9 +1128,6 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         ml[2 * c + 1] = nan ? __int_as_float(0x7fc00000) : l * pow2((float)-shift);
       }
     }
-    if (n > 1) wait_b(sm, &sm.pv[(n - 2) & 1], ((n - 2) >> 1) & 1, a);
-    wait_b(sm, &sm.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, a);
-    tc::fence_after_sync();
     tc::named_bar(bar_id, 128);
     float* o = a.part + ((unit * a.parts + part) * NC + c0) * kD + tok;
 #pragma unroll 1

@@ -506,6 +506,21 @@ def test_entries_out_of_range_are_latched(dtype):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [1, 8, 16, 40])
+def test_bad_page_at_the_end_of_a_long_tail(dtype, T):
+    """What is found wrong in a part's last tile makes all rows of the sequence NaN, in blocks of every size."""
+    pr = Problem(dtype=dtype, T=T, B=2, lens=[5000, 5000], page=64)
+    clean = pr.call()
+    api.pages_view(pr.pages, pr.state)["table"][1, 78] = pr.pages.n_pages
+    ws = torch.empty(api.tree_workspace_bytes(pr.p, 2, T, pr.pages), dtype=torch.uint8, device="cuda")
+    got = pr.call(workspace=ws)
+    assert torch.isnan(got[1]).all() and torch.equal(got[0], clean[0])
+    with pytest.raises(capi.AnchorKVError):
+        api.read_status(ws)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_deterministic_on_streams_and_in_graphs(dtype):
     """Two calls at once on two streams, and a captured call on new inputs, give the eager bits."""
     pr = Problem(dtype=dtype, T=6, lens=[100, 30], N=3000)
