@@ -102,6 +102,9 @@ __device__ __forceinline__ float p_target(int tiles) {
   return (float)min(kPMost, kPBits - 7 - (32 - __clz(tiles - 1)));   // 2^7 tokens a tile
 }
 constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
+// The sum's reference of a row that has met no logit: finite, so that a logit of
+// -inf beside it is still -inf and any other far above every limit.
+constexpr float kNoRef = -3.402823466e38f;
 constexpr float kRefGap = 120.f;          // the references' largest distance, either way
 // A part's sum is handed to the merge between 2^-12 and 2^-11, and its outputs in
 // the same unit: 2^11 parts of the largest finite values add up to a finite
@@ -758,11 +761,11 @@ __device__ __noinline__ void new_references(M& sm, const TreeArgs& a, uint32_t s
     const float l_old = -sm.nm[par][c], p_old = sm.mp[par][c];
     const float l_new = fmaxf(l_old, ceilf(m1));
     float p_new = fmaxf(p_old, ceilf(m2) + sm.target);
-    if (l_new > -INFINITY) p_new = fminf(fmaxf(p_new, l_new - kRefGap), l_new + kRefGap);   // cw is a normal number
-    sm.fl[par][c] = l_old > -INFINITY ? pow2(l_old - l_new) : 0.f;
+    if (l_new > kNoRef) p_new = fminf(fmaxf(p_new, l_new - kRefGap), l_new + kRefGap);   // cw is a normal number
+    sm.fl[par][c] = l_old > kNoRef ? pow2(l_old - l_new) : 0.f;
     sm.nm[par][c] = -l_new;
     sm.mp[par][c] = p_new;
-    sm.cw[par][c] = l_new > -INFINITY ? pow2(l_new - p_new) : 1.f;
+    sm.cw[par][c] = l_new > kNoRef ? pow2(l_new - p_new) : 1.f;
     __syncwarp(0xffffu);
     factor[tok] = p_old > -INFINITY ? pow2(p_old - p_new) : 0.f;
   }
@@ -866,7 +869,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
     const int r = blk * NC + tid;
     sm.colt[tid] = (unsigned char)min(r / a.G, a.T - 1);
     for (int i = 0; i < PG; ++i) {
-      sm.nm[i][tid] = INFINITY;
+      sm.nm[i][tid] = -kNoRef;
       sm.mp[i][tid] = -INFINITY;
       sm.cw[i][tid] = 1.f;
     }
@@ -1111,7 +1114,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
 #pragma unroll
       for (int k = 0; k < PG; ++k) {
         const float sum = sm.lsum[k][0][c] + sm.lsum[k][1][c] + sm.lsum[k][2][c] + sm.lsum[k][3][c];
-        l += sm.nm[k][c] < INFINITY ? sum * pow2(-sm.nm[k][c] - m) : sum;   // a sum without a reference is zero, or NaN
+        l += sm.nm[k][c] < -kNoRef ? sum * pow2(-sm.nm[k][c] - m) : sum;   // a sum without a reference is zero, or NaN
       }
       // the unit: a power of two, so that nothing is rounded
       const int shift = l > 0.f && l < INFINITY ? (__float_as_int(l) >> 23) - 126 + kSumBits : 0;
@@ -1119,7 +1122,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
       for (int k = 0; k < PG; ++k) {
         // two factors: one alone can be out of fp32's range, above it for values near their largest
         const float d = sm.mp[k][c] - m - (float)shift, half = floorf(0.5f * d);
-        const bool has = sm.nm[k][c] < INFINITY;
+        const bool has = sm.nm[k][c] < -kNoRef;
         fo[k * 32 + tok] = has ? pow2(half) : 0.f;
         fo[64 + k * 32 + tok] = pow2(d - half);
       }

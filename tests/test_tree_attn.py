@@ -423,6 +423,34 @@ def test_scales_of_tokens_and_residuals(dtype, gamma, sigma):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,T", [([0], 1), ([0], 4), ([130], 1), ([300], 6)])
+def test_seen_keys_whose_logits_are_minus_infinity(dtype, lens, T):
+    """A logit of -inf weighs nothing, also where it is all that a part of the tokens has for a row."""
+    pr = Problem(dtype=dtype, T=T, B=1, lens=lens, page=64)
+    pr.q[..., 0] = 1
+    word = [int(x) for x in pr.mask[0]]
+    last = T - 1
+    pr.mask[0] = torch.tensor([w & ~(1 << last) for w in word])
+    clean = pr.call()
+    masked, pr.mask = pr.mask, torch.tensor([word])
+    pr.Kn[0, last, :, 0] = -float("inf")
+    assert torch.equal(pr.call(), clean)                       # a draft: as if nobody saw it
+    table = api.pages_view(pr.pages, pr.state)["table"][0]
+    pages = table.tolist()
+    for j in pages[0:4:2] if lens[0] == 300 else pages[2:]:    # whole pages, or the last one's rows
+        pr.Kp[j, :, :, 0] = -float("inf")
+    got = pr.call().cpu().double()
+    rest = [1, 3, 4] if lens[0] == 300 else [0, 1]             # the pages that weigh anything
+    if lens[0]:
+        table[:len(rest)] = torch.tensor([pages[j] for j in rest])
+        pr.lens = [172 if lens[0] == 300 else 128]
+    pr.mask = masked
+    want, tol = pr.expect()
+    assert torch.isfinite(got).all() and ((got - want).norm(dim=3) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_infinity_in_a_committed_value(dtype):
     """All rows see it: its coordinate is not finite, the others are what they were."""
     pr = Problem(dtype=dtype, T=4, B=2, lens=[20, 9])
