@@ -91,7 +91,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // loss of all of them, n 2^-25, is then at most 2^-11 of that largest
 // contribution, one rounding of an operand.  What is left up to 2^15 is
 // headroom: a tile that passes it pays for new references, so it goes with the
-// part (17 bits for 2 k tokens, 13 for 32 k, 8 for 2^20).  Against 20 bits for
+// part (17 bits for 2 k tokens, 13 for 32 k).  Against 20 bits for
 // every part, which lost 1.6% of the output behind a first token 14 nats above
 // 32 k others and 5% of 128 k (graph, us; q scaled by 1 and 8): one draft 34.4,
 // 42.6 -> 34.8, 42.6; 64 drafts 116.4, 192 -> 122.5, 199; batch 16 475, 535 ->
@@ -1224,8 +1224,13 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
   //   192, 128 k           748    468    301    345
   //   32,  16 x 32 k       754    474    629
   //   64,  16 x 32 k      1397    891    639
-  constexpr int kRows[4] = {16, 32, 64, 128}, kTime[4] = {12, 14, 17, 29}, kSms = 148;
+  // A part has 64 k tokens at most (of either kind, about): every product of 16
+  // tokens may cut the accumulators by 2^-23, 4096 of them by 2^-11, the operands'
+  // own rounding.  2^20 tokens in one part behind a first one that takes 98% were
+  // off by 5.2e-3 of the output.
+  constexpr int kRows[4] = {16, 32, 64, 128}, kTime[4] = {12, 14, 17, 29}, kSms = 148, kMostTiles = (1 << 16) / kTT;
   const int pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (int)((tp->cap + tp->T + kTT - 1) / kTT);
+  const int least = std::max(prefix ? 2 : 1, (pre + tail + kMostTiles - 1) / kMostTiles);
   int64_t best = INT64_MAX;
   for (int k = 0; k < 4; ++k) {
     const int n_blk = (tp->rows + kRows[k] - 1) / kRows[k], units = tp->batch * pl.H * n_blk;
@@ -1234,7 +1239,7 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
     const int first = std::max(1, (units + kSms - 1) / kSms);
     for (int rounds = first; rounds < first + 12; ++rounds)
       for (int more = prefix; more >= 0; --more) {
-        const int parts = std::max(prefix ? 2 : 1, std::min(kSms * rounds / units + more, pre + tail));
+        const int parts = std::max(least, std::min(kSms * rounds / units + more, pre + tail));
         const int64_t cost = (run_length(units, parts, pre, tail) + run_length(units, parts, pre, 1)) * kTime[k];
         if (cost < best) {
           best = cost;

@@ -367,6 +367,36 @@ def test_sink_before_many_small_tokens(dtype, tokens, gap, spread, size):
 
 
 @gpu
+def test_sink_before_a_million_tokens():
+    """2^20 exact tokens, as many as page tables may reach, for as many sequences as there are SMs: what the sums of a
+    part round away stays below an operand's rounding.  The reference is on the GPU, in 64 bits."""
+    B, n, page, g = 148, 1 << 20, 128, torch.Generator(device="cuda").manual_seed(7)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")                                  # noqa: E731
+    u = rand(D)
+    u /= u.norm()
+    q = (8 * (u + 0.02 * rand(B, D))).bfloat16()
+    K = 0.3 * math.sqrt(D) / 8 * rand(n, 1) * u + 0.01 * rand(n, D)
+    K[0] = 18 * math.sqrt(D) / 8 * u
+    V = 1 + 0.3 * rand(n, D)
+    V[0] = rand(D)
+    K, V = K.bfloat16(), V.bfloat16()
+    spec = api.PageSpec(n_pages=n // page, page_size=page, n_slots=B, max_pages=n // page, n_kv_heads=1)
+    state = torch.zeros(spec.state_numel, dtype=torch.int32)
+    v = api.pages_view(spec, state)
+    v["len"][:] = n
+    v["table"][:] = torch.arange(spec.n_pages)
+    p = api.AnchorKVParams(n_tokens=1024, n_kv_heads=1, n_q_heads=1)
+    new = rand(B, 1, 1, D).bfloat16()
+    got = api.tree_attn(p, None, q[:, None, None], new, new, mask=torch.zeros(B, 1, dtype=torch.int64).cuda(), pages=spec,
+                        state=state.cuda(), K_pages=K.reshape(-1, 1, page, D), V_pages=V.reshape(-1, 1, page, D))[:, 0, 0].double()
+    k, x = K.double(), V.double()
+    for i in range(0, B, 37):
+        want, tol = sink_tolerance(q[i:i + 37].double(), k, x, k.norm(dim=1), x.norm(dim=1), 2.0 ** -11, 0, 2.0 ** -8)
+        off = (got[i:i + 37] - want).norm(dim=1)
+        assert (off <= tol).all(), (off / tol).max()
+
+
+@gpu
 def test_sink_of_a_compressed_prompt():
     """The same behind a compressed prompt, whose rows are rounded like all others."""
     H, B, N, g = 4, 37, 32768, torch.Generator().manual_seed(6)
