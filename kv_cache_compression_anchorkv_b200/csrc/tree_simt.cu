@@ -9,7 +9,12 @@
 // into shared memory, then 256 threads take the logits, the running maximum and
 // sum of the softmax, and the products with the values, which stay in
 // registers.  Everything is held in 32 bits: an fp32 cache is answered in fp32
-// accuracy, which the tensor cores' operand types are short of.
+// accuracy.  A tile's 32 terms are summed by themselves and join the row's sums
+// with the rounding kept in a second word, since a part may be a million tokens
+// long: added one by one behind a token that takes nearly all, 128 k small ones
+// were off by 9e-4 of the output and 2^20 by 6e-3 (4e-7 now, for 9% of the time of
+// blocks of 64 rows and 2% of 16; the second words are in shared memory, in
+// registers they spilled and took 20%).
 // Sixteen rows serve single tokens and small trees, where the latency of one
 // tile counts; 64 rows share a rebuilt tile and read shared memory six times
 // for 32 multiplications (logits) and three times (values), against three and
@@ -38,7 +43,7 @@ struct Sm {
   float K[kTT][kKPitch];
   float V[kTT][kD];
   float P[kTT][RB + 4];
-  float scale[RB];
+  float low[RB][kD];                                  // what the output rows' sums rounded away
   unsigned long long mask[RB];
 };
 
@@ -94,6 +99,16 @@ __device__ __forceinline__ Item find_item(const TreeArgs& a, const uint8_t* comp
   return it;
 }
 
+// sum + low += x with the rounding of the sum kept in `low` (Knuth's two-sum): a
+// tile's share joins a long sum without a loss, however small it is beside it.
+__device__ __forceinline__ void add_exactly(float& sum, float& low, float x) {
+  const float t = sum + x, z = t - sum;
+  low += (sum - (t - z)) + (x - z);
+  sum = t;
+}
+// Their value; an infinite sum has no rounding.
+__device__ __forceinline__ float together(float sum, float low) { return fabsf(low) < INFINITY ? sum + low : sum; }
+
 template <int kRB>
 __global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
   constexpr int kRW = kRB / 8;                        // rows of a warp in the softmax and the values' products
@@ -127,13 +142,15 @@ __global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
   }
   float acc[kRW][4];                                  // four columns of each row
 #pragma unroll
-  for (int i = 0; i < kRW; ++i)
+  for (int i = 0; i < kRW; ++i) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    *reinterpret_cast<float4*>(&sm.low[kRW * warp + i][lane * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   // softmax state of the warp's rows, the same in every lane
-  float m[kRW], l[kRW];
+  float m[kRW], l[kRW], l_low[kRW];
 #pragma unroll
-  for (int i = 0; i < kRW; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+  for (int i = 0; i < kRW; ++i) { m[i] = -INFINITY; l[i] = l_low[i] = 0.f; }
   __shared__ int bad_page;
   if (tid == 0) bad_page = 0;
   __syncthreads();
@@ -224,6 +241,7 @@ __global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
     // softmax: lane = token.  Masked places of a tile with drafts become -1, so
     // that the products leave them out whatever the value's row holds; tokens
     // behind the last have zero rows.
+    float sum[kRW][4];                                     // of this tile
     const int u = tt + lane - n_pre - len;                 // draft index, negative before the drafts
     const bool drafts = tt + nt > n_pre + len;
 #pragma unroll
@@ -235,11 +253,19 @@ __global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
       const float mn = fmaxf(m[i], warp_max(off ? -INFINITY : s));
       const float sc = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
       const float p = off ? 0.f : (mn == -INFINITY && s == mn) ? 0.f : exp2f(s - mn);
-      l[i] = l[i] * sc + warp_sum(p);
+      if (sc != 1.f) {                                     // the same for the whole warp
+        l[i] *= sc;
+        l_low[i] *= sc;
+        float4* low = reinterpret_cast<float4*>(&sm.low[r][lane * 4]);
+        *low = make_float4(low->x * sc, low->y * sc, low->z * sc, low->w * sc);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] *= sc;
+      }
+      add_exactly(l[i], l_low[i], warp_sum(p));
       m[i] = mn;
       sm.P[lane][r] = off && drafts ? -1.f : p;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] *= sc;
+      for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
     }
     __syncwarp();                                          // the warp's own rows
     if (drafts) {
@@ -249,10 +275,10 @@ __global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
         for (int i = 0; i < kRW; ++i) {
           const float p = sm.P[j][kRW * warp + i];
           if (p < 0.f) continue;
-          acc[i][0] = fmaf(p, v.x, acc[i][0]);
-          acc[i][1] = fmaf(p, v.y, acc[i][1]);
-          acc[i][2] = fmaf(p, v.z, acc[i][2]);
-          acc[i][3] = fmaf(p, v.w, acc[i][3]);
+          sum[i][0] = fmaf(p, v.x, sum[i][0]);
+          sum[i][1] = fmaf(p, v.y, sum[i][1]);
+          sum[i][2] = fmaf(p, v.z, sum[i][2]);
+          sum[i][3] = fmaf(p, v.w, sum[i][3]);
         }
       }
     } else {
@@ -268,12 +294,22 @@ __global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < kRW; ++i) {
-          acc[i][0] = fmaf(p[i], v.x, acc[i][0]);
-          acc[i][1] = fmaf(p[i], v.y, acc[i][1]);
-          acc[i][2] = fmaf(p[i], v.z, acc[i][2]);
-          acc[i][3] = fmaf(p[i], v.w, acc[i][3]);
+          sum[i][0] = fmaf(p[i], v.x, sum[i][0]);
+          sum[i][1] = fmaf(p[i], v.y, sum[i][1]);
+          sum[i][2] = fmaf(p[i], v.z, sum[i][2]);
+          sum[i][3] = fmaf(p[i], v.w, sum[i][3]);
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kRW; ++i) {
+      float4* low = reinterpret_cast<float4*>(&sm.low[kRW * warp + i][lane * 4]);
+      float4 x = *low;
+      add_exactly(acc[i][0], x.x, sum[i][0]);
+      add_exactly(acc[i][1], x.y, sum[i][1]);
+      add_exactly(acc[i][2], x.z, sum[i][2]);
+      add_exactly(acc[i][3], x.w, sum[i][3]);
+      *low = x;
     }
     bad = __syncthreads_or(bad_page);                  // the same answer for all: nobody looks at the next tile yet
   }
@@ -284,9 +320,11 @@ __global__ void __launch_bounds__(kThr, 2) tree_simt_kernel(TreeArgs a) {
     if (lane == 0) {
       // a sequence that could not be read is NaN, not a guess
       ml[2 * r] = bad ? __uint_as_float(kTreeBadPart) : m[i];
-      ml[2 * r + 1] = bad ? __int_as_float(0x7fc00000) : l[i];
+      ml[2 * r + 1] = bad ? __int_as_float(0x7fc00000) : together(l[i], l_low[i]);
     }
-    *reinterpret_cast<float4*>(o + i * kD) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    const float4 x = *reinterpret_cast<const float4*>(&sm.low[r][lane * 4]);
+    *reinterpret_cast<float4*>(o + i * kD) =
+        make_float4(together(acc[i][0], x.x), together(acc[i][1], x.y), together(acc[i][2], x.z), together(acc[i][3], x.w));
   }
 }
 

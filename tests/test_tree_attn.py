@@ -328,7 +328,7 @@ def sink_tolerance(q, K, V, Kn, Vn, u, n, half):
 
 
 @gpu
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("tokens,gap,spread,size", [
     (32768, 14.0, 0.3, 1.0), (32768, 16.0, 0.3, 0.1), (32768, 14.0, 1.0, 1.0), (131072, 14.0, 0.3, 1.0),
     (131072, 16.0, 1.0, 0.1), (131072, 17.0, 0.1, 0.3)])
