@@ -440,8 +440,13 @@ typedef struct anchorkv_tree {
   void* out;                 /* device [batch][T][H_q][D] dtype; rows t >= n_new[b] stay as they are */
 } anchorkv_tree;
 
-/* Workspace bytes anchorkv_tree_attn needs for `batch` sequences of `n_draft`
- * drafts; pg may be NULL (no exact tokens).  Host, pure. */
+/* Workspace bytes of anchorkv_tree_attn for `batch` sequences of `n_draft`
+ * drafts; pg may be NULL (no exact tokens).  They serve every call of as many
+ * sequences and drafts or fewer.  Such a call may have more bytes of its own,
+ * since few rows are divided into more parts; in a workspace that is short of
+ * those its tokens are divided into fewer, with other roundings and somewhat
+ * slower, so a program that wants each call at its best takes the largest of its
+ * sizes' bytes.  Host, pure. */
 int anchorkv_tree_workspace_bytes(const anchorkv_params* p, int32_t batch, int32_t n_draft,
                                   const anchorkv_pages* pg, size_t* ws_bytes);
 

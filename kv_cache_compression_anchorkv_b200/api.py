@@ -408,6 +408,8 @@ def pages_compact(pages: PageSpec, state: torch.Tensor, K_pages: torch.Tensor, V
 
 
 def tree_workspace_bytes(p: AnchorKVParams, batch: int, drafts: int, pages: PageSpec | None = None) -> int:
+    """Scratch of tree_attn for this many sequences and drafts; it serves fewer
+    of either too, though such a call's own bytes may be more and make it faster."""
     n = ctypes.c_size_t()
     pg = ctypes.byref(pages.c()) if pages is not None else None
     capi.check("anchorkv_tree_workspace_bytes",

@@ -19,6 +19,7 @@ struct TreePlan {
   int batch, T, rows, RB, n_blk, parts;
   int tail_parts;                    // of those, CTAs of exact tokens only; 0: by the sequence's lengths
   int64_t cap;                       // exact tokens that the page tables can hold
+  int64_t room;                      // part rows (sequence, head, block, part, row) that the workspace has room for
   // workspace (bytes): status words, (max, sum) and outputs of every
   // part; tensor-core kernel: rotated anchors, their scales, token tables,
   // infinite values

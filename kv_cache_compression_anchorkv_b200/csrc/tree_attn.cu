@@ -7,8 +7,14 @@
 namespace akv {
 namespace {
 
-int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pages* pg, bool prefix, Plan* pl,
-                   TreePlan* tp) {
+constexpr int64_t kAnyBytes = (int64_t)1 << 60;
+
+// The plan for a workspace of ws_bytes.  The best division of the tokens may need
+// more bytes for fewer rows or sequences; where it does not fit, the tokens are
+// divided into as many parts as do, so that what serves a call serves every
+// smaller one: with its own blocks and `least` parts that needs no more.
+int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pages* pg, bool prefix, int64_t ws_bytes,
+                   Plan* pl, TreePlan* tp) {
   int st = make_plan(p, pl);
   if (st) return st;
   if (batch < 0 || T < 1 || T > kTreeMaxDrafts) return ANCHORKV_EINVAL;
@@ -25,13 +31,8 @@ int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pa
   }
   // bf16 caches on the tensor cores; fp32 caches need 32-bit products
   const bool tcore = p->dtype == ANCHORKV_BF16;
-  if (tcore) tree_plan_tc(*pl, prefix, tp);
-  else tree_plan_simt(*pl, tp);
-  const int64_t parts = (int64_t)tp->batch * pl->H * tp->n_blk * tp->parts * tp->RB;
   int64_t off = 256;                                                     // status words
   auto take = [&](int64_t bytes) { const int64_t o = off; off += (bytes + 255) / 256 * 256; return o; };
-  tp->o_ml = take(8 * parts);
-  tp->o_part = take(4 * kD * parts);
   if (tcore) {
     const int64_t rows = (int64_t)tp->batch * 2 * pl->H * pl->k;
     tp->o_anc = take(2 * kD * rows);
@@ -39,6 +40,14 @@ int make_tree_plan(const anchorkv_params* p, int batch, int T, const anchorkv_pa
     if (prefix) tp->o_meta = take(tree_meta_bytes() * tp->batch * 2 * pl->H * pl->n_tiles);
     tp->o_inf = take(8 * (int64_t)tp->batch * pl->H);
   }
+  // rows come in blocks of 16 at least: 128 bytes of (max, sum) and 8 KB of outputs
+  tp->room = std::max<int64_t>(0, (ws_bytes - off) / (16 * (8 + 4 * kD)) * 16);
+  if (tp->room % 32 && off + tp->room * (8 + 4 * kD) + 128 > ws_bytes) tp->room -= 16;     // (max, sum) padded to 256
+  if (tcore) tree_plan_tc(*pl, prefix, tp);
+  else tree_plan_simt(*pl, tp);
+  const int64_t parts = (int64_t)tp->batch * pl->H * tp->n_blk * tp->parts * tp->RB;
+  tp->o_ml = take(8 * parts);
+  tp->o_part = take(4 * kD * parts);
   tp->ws_total = off;
   return ANCHORKV_OK;
 }
@@ -58,7 +67,7 @@ int anchorkv_tree_workspace_bytes(const anchorkv_params* p, int32_t batch, int32
   // the split differs with and without compressed tokens
   int64_t most = 0;
   for (const bool prefix : {true, false}) {
-    const int st = make_tree_plan(p, batch, n_draft, pg, prefix, &pl, &tp);
+    const int st = make_tree_plan(p, batch, n_draft, pg, prefix, kAnyBytes, &pl, &tp);
     if (st) return st;
     most = std::max(most, tp.ws_total);
   }
@@ -70,7 +79,8 @@ int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* w
   if (!t) return ANCHORKV_EINVAL;
   Plan pl;
   TreePlan tp;
-  int st = make_tree_plan(p, t->batch, t->n_draft, t->pages, t->compressed != nullptr, &pl, &tp);
+  int st = make_tree_plan(p, t->batch, t->n_draft, t->pages, t->compressed != nullptr, (int64_t)std::min<size_t>(ws_bytes, kAnyBytes),
+                          &pl, &tp);
   if (st) return st;
   if (t->batch == 0) return ANCHORKV_OK;
   if (!t->q || !t->K_new || !t->V_new || !t->out || !ws) return ANCHORKV_EINVAL;

@@ -361,7 +361,8 @@ void tree_plan_simt(const Plan& pl, TreePlan* tp) {
   tp->n_blk = (tp->rows + tp->RB - 1) / tp->RB;
   // parts so that two CTAs an SM have work, of a tile at least
   const int64_t units = (int64_t)tp->batch * pl.H * tp->n_blk;
-  tp->parts = tp->tail_parts = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (2 * 148 + units - 1) / units));
+  const int64_t fit = tp->room / (units * tp->RB);
+  tp->parts = tp->tail_parts = (int)std::max<int64_t>(1, std::min(std::min(tiles, fit), (2 * 148 + units - 1) / units));
 }
 
 int launch_tree_simt(const TreeArgs& a, cudaStream_t s) { return a.RB == 16 ? launch_rb<16>(a, s) : launch_rb<64>(a, s); }

@@ -65,6 +65,7 @@
 // finding the residuals' levels before the rows have landed was slower (36.5 ->
 // 39 us on one draft): the registers and second pass cost more than the wait.
 
+#include <limits.h>
 #include <stddef.h>
 
 #include <algorithm>
@@ -1232,6 +1233,10 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
   const int pre = prefix ? (pl.N + kTT - 1) / kTT : 0, tail = (int)((tp->cap + tp->T + kTT - 1) / kTT);
   const int least = std::max(prefix ? 2 : 1, (pre + tail + kMostTiles - 1) / kMostTiles);
   int64_t best = INT64_MAX;
+  tp->RB = kRows[0];                                   // where nothing fits: the caller finds the workspace too small
+  tp->n_blk = (tp->rows + tp->RB - 1) / tp->RB;
+  tp->parts = least;
+  tp->tail_parts = prefix ? 0 : least;
   for (int k = 0; k < 4; ++k) {
     const int n_blk = (tp->rows + kRows[k] - 1) / kRows[k], units = tp->batch * pl.H * n_blk;
     // as many parts of compressed tokens (with and without one of exact tokens
@@ -1239,7 +1244,9 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
     const int first = std::max(1, (units + kSms - 1) / kSms);
     for (int rounds = first; rounds < first + 12; ++rounds)
       for (int more = prefix; more >= 0; --more) {
-        const int parts = std::max(least, std::min(kSms * rounds / units + more, pre + tail));
+        const int fit = (int)std::min<int64_t>(tp->room / ((int64_t)units * kRows[k]), INT_MAX);
+        if (fit < least) continue;
+        const int parts = std::min(fit, std::max(least, std::min(kSms * rounds / units + more, pre + tail)));
         const int64_t cost = (run_length(units, parts, pre, tail) + run_length(units, parts, pre, 1)) * kTime[k];
         if (cost < best) {
           best = cost;

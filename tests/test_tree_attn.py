@@ -768,3 +768,31 @@ def test_null_arguments_refused():
     assert capi.lib().anchorkv_tree_attn(ctypes.byref(p.c()), None, FAKE, 1 << 30, None) == capi.EINVAL
     assert capi.lib().anchorkv_tree_workspace_bytes(ctypes.byref(p.c()), 1, 1, None, None) == capi.EINVAL
     assert capi.lib().anchorkv_tree_workspace_bytes(None, 1, 1, None, ctypes.byref(n)) == capi.EINVAL
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("prefix", [True, False])
+def test_a_workspace_serves_smaller_calls(dtype, prefix):
+    """What a program takes for its largest tree and batch is enough for all others."""
+    p = api.AnchorKVParams(n_tokens=32768, n_kv_heads=8, n_q_heads=32, dtype=dtype)
+    spec = api.PageSpec(n_pages=64, page_size=64, n_slots=40, max_pages=32, n_kv_heads=8, dtype=dtype)
+    kw = dict(p=p, spec=spec, q_tok_stride=4096, q_seq_stride=4096 * 64, new_tok_stride=1024, new_seq_stride=1024 * 64,
+              n_layouts=40, seq_stride_bytes=1 << 30, **({} if prefix else dict(compressed=None)))
+    for batch, drafts in ((8, 64), (4, 48), (40, 64), (40, 3), (19, 40), (37, 17)):
+        size = api.tree_workspace_bytes(p, batch, drafts, spec)
+        assert host_call(batch=batch, n_draft=drafts, ws_bytes=size, **kw) != capi.ENOSPC
+        for b in range(1, batch + 1):
+            for t in range(1, drafts + 1):
+                assert host_call(batch=b, n_draft=t, ws_bytes=size, **kw) != capi.ENOSPC, (batch, drafts, b, t)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,N,B,T", [("fp32", 3000, 5, 48), ("bf16", 5000, 3, 32)])
+def test_small_calls_in_the_workspace_of_a_large_one(dtype, N, B, T):
+    """Fewer parts than the call would have by itself: the same answer, inside the same bytes."""
+    small = Problem(dtype=dtype, H=8, G=4, N=N, B=B, layouts=1, T=T, lens=[300, 20, 7, 0, 64][:B], page=64)
+    own, size = (api.tree_workspace_bytes(small.p, B, t, small.pages) for t in (T, T + 1))
+    assert size < own
+    ws = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+    small.check(out=small.call(workspace=ws[:size]))
+    assert (ws[size:] == 77).all()
