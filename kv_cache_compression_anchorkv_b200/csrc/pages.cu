@@ -608,8 +608,9 @@ int anchorkv_pages_commit(const anchorkv_pages* pg, const int32_t* state_in, int
   PgArgs a;
   int st = make_args(pg, &a);
   if (st) return st;
-  if (batch < 0 || batch > a.S || n_draft < 1 || n_draft > 65536 || !n_accept) return ANCHORKV_EINVAL;
-  if (!K_new || !V_new || (((uintptr_t)K_new | (uintptr_t)V_new) & 15)) return ANCHORKV_EINVAL;
+  if (batch < 0 || batch > a.S || n_draft < 1 || n_draft > 65536) return ANCHORKV_EINVAL;
+  if (batch > 0 && (!K_new || !V_new || !n_accept)) return ANCHORKV_EINVAL;       // of no sequences there are no rows
+  if ((((uintptr_t)K_new | (uintptr_t)V_new) & 15)) return ANCHORKV_EINVAL;
   if (((uintptr_t)path | (uintptr_t)n_accept) & 3) return ANCHORKV_EINVAL;
   st = op_args(pg, state_in, state_out, K_pages, V_pages, ws, ws_bytes, &a);
   if (st) return st;

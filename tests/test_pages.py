@@ -162,6 +162,20 @@ def test_fewer_sequences_than_slots():
 
 
 @gpu
+@pytest.mark.parametrize("in_place", [True, False])
+def test_commit_of_no_sequences(in_place):
+    """A step in which no sequence is left: the state is as it was."""
+    spec = SPECS[0]
+    g, K, V = make(spec)
+    m, Kg, Vg = Model(spec, K, V), K.cuda(), V.cuda()
+    state = api.pages_init(spec)
+    Kn, Vn = drafts(spec, 0, 5, g)
+    got = api.pages_commit(spec, state, Kg, Vg, Kn.cuda(), Vn.cuda(), i32([]), path=i32([]).reshape(0, 5),
+                           state_out=None if in_place else torch.full_like(state, -7))
+    m.same(got, Kg, Vg)
+
+
+@gpu
 def test_many_slots_and_wide_tables():
     """More slots than threads of the state kernels, and a table far wider than what is used."""
     spec = api.PageSpec(n_pages=5000, page_size=16, n_slots=2100, max_pages=300, n_layers=1, n_kv_heads=1)
@@ -418,6 +432,12 @@ def test_bad_commit_arguments_refused(at, value, status):
     args = [FAKE, FAKE, FAKE + 4096, FAKE + 8192, FAKE, FAKE, 4, 2, None, FAKE, FAKE, 1 << 20]
     args[at] = value
     assert call("anchorkv_pages_commit", ctypes.byref(spec.c()), *args, None) == status
+
+
+def test_commit_of_no_sequences_needs_no_rows():
+    spec = api.PageSpec(n_pages=8, n_slots=4)
+    args = [FAKE, FAKE, FAKE + 4096, FAKE + 8192, 0, 0, 0, 2, None, 0, FAKE, 64]
+    assert call("anchorkv_pages_commit", ctypes.byref(spec.c()), *args, None) == capi.ENOSPC        # the next check
 
 
 @pytest.mark.parametrize("at,value,status", [(0, 0, capi.EINVAL), (1, 0, capi.EINVAL), (2, 0, capi.EINVAL),
