@@ -107,8 +107,8 @@ constexpr float kSumLimit = 1.0995116e12f;  // 2^40, far below fp32's range
 // -inf beside it is still -inf and any other far above every limit.
 constexpr float kNoRef = -3.402823466e38f;
 constexpr float kRefGap = 120.f;          // the references' largest distance, either way
-// A part's sum is handed to the merge between 2^-12 and 2^-11, and its outputs in
-// the same unit: 2^11 parts of the largest finite values add up to a finite
+// A part's sum is handed to the merge between 2^-12 and 2^-11 (logits beyond 2^23
+// aside), and its outputs in the same unit: 2^11 parts of the largest finite values add up to a finite
 // number, and a bf16 output keeps its bits down to the smallest normal one.
 constexpr int kSumBits = 11;
 
@@ -1117,8 +1117,9 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1) tree_tc_kernel(TreeArg
         const float sum = sm.lsum[k][0][c] + sm.lsum[k][1][c] + sm.lsum[k][2][c] + sm.lsum[k][3][c];
         l += sm.nm[k][c] < -kNoRef ? sum * pow2(-sm.nm[k][c] - m) : sum;   // a sum without a reference is zero, or NaN
       }
-      // the unit: a power of two, so that nothing is rounded
-      const int shift = l > 0.f && l < INFINITY ? (__float_as_int(l) >> 23) - 126 + kSumBits : 0;
+      // the unit: a power of two, so that nothing is rounded, and none where the
+      // reference plus its exponent would not be a whole number in fp32
+      const int shift = l > 0.f && l < INFINITY && fabsf(m) < 8388608.f ? (__float_as_int(l) >> 23) - 126 + kSumBits : 0;
 #pragma unroll
       for (int k = 0; k < PG; ++k) {
         // two factors: one alone can be out of fp32's range, above it for values near their largest

@@ -312,6 +312,26 @@ def test_finite_values_near_the_ends_of_their_type(scale, T):
         assert (off <= tol + 2.0 ** -134 * math.sqrt(D)).all(), (off / tol).max()
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("size", [1.0, 64.0, 2048.0, 32768.0])
+@pytest.mark.parametrize("T", [1, 20])
+def test_equal_logits_of_any_size(dtype, size, T):
+    """Tokens with one and the same key weigh alike, in parts of unequal length and however large the logit is (up to
+    1e10, where fp32 counts in steps of 1024): the output is the mean of the values.  Errors: a value's row, 2^-11 of
+    it (fp32: the sums' 128 terms), and the output's half step."""
+    n = 1000
+    pr = Problem(dtype=dtype, T=T, B=1, lens=[n], page=64, prefix=False, mask=torch.zeros(1, T, dtype=torch.int64))
+    pr.q = torch.full_like(pr.q, size)
+    pr.Kp = torch.full_like(pr.Kp, size)
+    got = pr.call()[0].cpu().double()
+    table = api.pages_view(pr.pages, pr.state)["table"][0].long()
+    V = pr.Vp[table].double().permute(1, 0, 2, 3).reshape(pr.H, -1, D)[:, :n].repeat_interleave(pr.G, 0)
+    u, half = (129 * 2.0 ** -24, 2.0 ** -24) if dtype == "fp32" else (2.0 ** -11, 2.0 ** -8)
+    want, tol = V.mean(1), u * V.norm(dim=2).mean(1) + half * V.mean(1).norm(dim=1)
+    assert ((got - want).norm(dim=2) <= tol).all(), ((got - want).norm(dim=2) / tol).max()
+
+
 def sink_tolerance(q, K, V, Kn, Vn, u, n, half):
     """(outputs, tolerance) of rows q over tokens K, V, with a logit's error counted token by token.
 
