@@ -453,7 +453,7 @@ int anchorkv_tree_workspace_bytes(const anchorkv_params* p, int32_t batch, int32
 /*
  * Runs the attention above on `stream`.  Every device pointer is 16-byte
  * aligned, and so is every row that the strides reach (EINVAL otherwise); D is
- * contiguous and heads are D apart.  The call overwrites `ws`, whose first
+ * contiguous, heads are D apart and tokens a row of all heads or more.  The call overwrites `ws`, whose first
  * words are a status word and counters: a layout_of or page-table entry out of
  * its range latches code 3 there (anchorkv_read_device_status) and the rows of
  * that sequence become NaN; code 4 is a bounded wait that timed out.  Calls
@@ -462,7 +462,9 @@ int anchorkv_tree_workspace_bytes(const anchorkv_params* p, int32_t batch, int32
  * than 2^20 tokens.
  * bf16 caches: logits and values on the tensor cores with fp16 operands (rows
  * over powers of two) and fp32 accumulators, sums and scales; the output is
- * rounded once.  fp32 caches: fp32 throughout.  Output is bit-for-bit
+ * rounded once and off by about 2^-9 of its size in all, a little more than its
+ * own rounding.  fp32 caches: fp32 throughout; values are summed before they
+ * are divided, so finite ones above 2^107 may overflow.  Output is bit-for-bit
  * deterministic.
  */
 int anchorkv_tree_attn(const anchorkv_params* p, const anchorkv_tree* t, void* ws, size_t ws_bytes, void* stream);

@@ -438,7 +438,8 @@ def tree_attn(p: AnchorKVParams, compressed: torch.Tensor | None, q: torch.Tenso
               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Attention for a tree of drafted tokens (anchorkv_tree_attn).
     q: [batch, T, H_q, D] and K_new, V_new: [batch, T, H, D] of the drafts, T <= 64
-    (sequence and token strides are free, e.g. slices of a fused projection);
+    (sequence strides are free and token strides from a row of all heads up,
+    e.g. slices of a fused projection);
     compressed: uint8 [n_layouts, stride] or [total_bytes], or None;
     layout_of: int32 [batch], the layout of each sequence (default: b);
     n_new: int32 [batch], drafts of each sequence (default T); mask: int64

@@ -15,10 +15,10 @@
 // ready.  Ids are handed out by scans in slot or page order, never by
 // atomics, so they depend on the state alone.
 //
-// Measured (CUDA graph, bf16, 32 layers of 8 heads): one token 6.2 us and the
-// last pages of 4 beams 10.5 us (two launches and the state kernel's scans
-// bound them), 16 accepted paths of up to 16 rows 16.8 us (3.3 TB/s), 64 slots
-// forked 22.6 us (4.2 TB/s), 40 of 160 pages moved 112 us (6.0 TB/s, 91% of a
+// Measured (CUDA graph, bf16, 32 layers of 8 heads): one token 6.8 us and the
+// last pages of 4 beams 11.1 us (two launches and the state kernel's scans
+// bound them), 16 accepted paths of up to 16 rows 17.2 us (3.2 TB/s), 64 slots
+// forked 24.4 us (3.9 TB/s), 40 of 160 pages moved 114 us (5.9 TB/s, 90% of a
 // copy's rate).
 #include <algorithm>
 

@@ -21,7 +21,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&c)[4]) {
 // Four warps per output row, each a quarter of the parts: joined by their
 // references and sums, the compressed tokens' share rotated back.  Bound by the
 // latency of the parts' reads from L2, so they are spread over warps: 2.5 us
-// inside a call for 32 rows of 19 parts, 11 us for 2048 rows of 9 (9.4 MB).
+// inside a call for 32 rows of 19 parts, 11 to 13 us for 2048 rows of 9 (9.4 MB).
 template <typename T>
 __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int rb) {
   __shared__ float4 sum[2][4][2][32];

@@ -19,9 +19,9 @@
 // tile counts; 64 rows share a rebuilt tile and read shared memory six times
 // for 32 multiplications (logits) and three times (values), against three and
 // two for eight, and are bound by those multiplications.  Measured: 1024 tokens,
-// one head of 20 rows 17.4 us (latency: a tile after another, then the merge);
-// four sequences, eight heads, 8192 tokens, 64 rows 743 us in blocks of 64 and
-// 1617 in blocks of 16 (12 TFLOP/s of fp32); two, 512 rows 2.50 ms and 5.54.
+// one head of 20 rows 18.2 us (latency: a tile after another, then the merge);
+// four sequences, eight heads, 8192 tokens, 64 rows 785 us in blocks of 64 and
+// 1595 in blocks of 16 (11 TFLOP/s of fp32); two, 512 rows 2.63 ms and 5.38.
 #include <algorithm>
 #include <mutex>
 
@@ -352,9 +352,9 @@ int launch_rb(const TreeArgs& a, cudaStream_t s) {
 
 void tree_plan_simt(const Plan& pl, TreePlan* tp) {
   // 64 rows where an SM has a tile of such a block at least.  Measured (16 rows,
-  // 64 rows; us): one head of 64 rows, 1 k tokens 17.7, 28.8; 8 k 52.8, 46.2;
-  // eight heads of 64 rows, 1 k 50.9, 34.7; 4 k 243, 84; eight of 20, 1 k 29.3,
-  // 28.3; 8 k 195, 127
+  // 64 rows; us): one head of 64 rows, 1 k tokens 18.9, 30.6; 8 k 54.9, 49.2;
+  // eight heads of 64 rows, 1 k 52.8, 37.6; 4 k 248, 91; eight of 20, 1 k 31.1,
+  // 31.1; 8 k 199, 136
   const int64_t tiles = (pl.N + tp->cap + tp->T + kTT - 1) / kTT;
   const bool wide = tp->rows > 16 && (int64_t)tp->batch * pl.H * ((tp->rows + 63) / 64) * tiles >= 148;
   tp->RB = wide ? 64 : 16;

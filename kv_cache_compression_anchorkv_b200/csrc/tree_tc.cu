@@ -52,14 +52,14 @@
 // tile costs about 4.6 k warp instructions (softmax 1 k, residual rows 1 k,
 // the rest copies and waits) and 2.2 k cycles; the anchor rows then come from
 // L2 at 6.5 TB/s (64 KB a tile).  For 128 rows it is the softmax: 16 warps, 11 k
-// warp instructions and 5 k cycles a tile, 56% of the issue slots.
+// warp instructions and 5 k cycles a tile, 55% of the issue slots.
 // Whole calls (CUDA graph, 8 KV heads, theta = 0.05), with the rate of
 // 4 D operations a row and token:
-//   32 k tokens, 32 query heads: 1 draft 34.0 us (210 GB/s of the layout: three
+//   32 k tokens, 32 query heads: 1 draft 36.1 us (198 GB/s of the layout: three
 //     fifths are the pre-kernels, the first tile and the merge), 16 drafts
-//     45.4 us (191 TFLOP/s), 64 drafts 116.4 us (304 TFLOP/s)
-//   128 k tokens, 64 query heads, 24 drafts: 301 us (344 TFLOP/s)
-//   16 sequences of 32 k tokens, theta = 0.1, 8 drafts: 474 us (533 GB/s)
+//     47.3 us (184 TFLOP/s), 64 drafts 123.7 us (286 TFLOP/s)
+//   128 k tokens, 64 query heads, 24 drafts: 315 us (329 TFLOP/s)
+//   16 sequences of 32 k tokens, theta = 0.1, 8 drafts: 480 us (526 GB/s)
 // Anchor rows by four-row TMA gathers were no faster than 16-byte copies (60.4
 // us against 59.8 on 16 drafts then: about 100 cycles of issue a gather);
 // finding the residuals' levels before the rows have landed was slower (36.5 ->
@@ -1219,13 +1219,14 @@ void tree_plan_tc(const Plan& pl, bool prefix, TreePlan* tp) {
   // rows; smaller ones leave less of a block empty and spread over more SMs.
   // Measured (8 KV heads, us; each at its own best parts):
   //   rows a head, block of  16     32     64    128
-  //   24,  32 k tokens      51.0   39.5
-  //   64,  32 k             85.3   60.9   45.4
-  //   128, 32 k            151    102     72.0   70.0
-  //   256, 32 k            286    187    125    116
-  //   192, 128 k           748    468    301    345
-  //   32,  16 x 32 k       754    474    629
-  //   64,  16 x 32 k      1397    891    639
+  //   4,   32 k tokens      36.7   40.5   45.6   65.5
+  //   24,  32 k             54.1   40.8   46.0   65.5
+  //   64,  32 k             89.2   63.2   47.4   68.5
+  //   128, 32 k            157    106     75.8   74.1
+  //   256, 32 k            294    191    130    124
+  //   192, 128 k           792    477    315    369
+  //   32,  16 x 32 k       762    480    630    795
+  //   64,  16 x 32 k      1412    911    641    815
   // A part has 64 k tokens at most (of either kind, about): every product of 16
   // tokens may cut the accumulators by 2^-23, 4096 of them by 2^-11, the operands'
   // own rounding.  2^20 tokens in one part behind a first one that takes 98% were
